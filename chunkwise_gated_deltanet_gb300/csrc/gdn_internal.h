@@ -164,6 +164,77 @@ cudaError_t launch_state_fold(const float* S_in, const float* M, const float* L,
 long long decode_ctas(long long N, long long H, int dk, int dv);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 
+// Records the message gdn_last_error() returns on this host thread; returns `code`.
+int set_error(int code, const char* fmt, ...);
+
+// Serving operators, already validated by the API layer.
+struct PlanArgs {
+  const int32_t* context_lens;  // [N]
+  const int32_t* new_lens;      // [N]
+  int32_t* block_tables;        // [N, max_blocks]
+  int32_t* free_ring;           // [num_blocks]
+  const int32_t* ring_in;       // {head, count}
+  int32_t* ring_out;
+  int32_t* cu_seqlens;          // [N + 1]
+  int32_t* seq_lens;            // [N]
+  int32_t* slot_map;            // [T]
+  int32_t* positions;           // [T]
+  int32_t* granted;             // [N]
+  int N, T, max_blocks, num_blocks, block_size;
+};
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream);
+
+struct WriteArgs {
+  const void* k;
+  const void* v;
+  const int32_t* slot_map;
+  void* k_cache;
+  void* v_cache;
+  long long k_stride, v_stride;  // bytes between tokens
+  int T, row_bytes;              // bytes of one token's heads, a multiple of 16
+  long long slots;               // num_blocks * block_size
+};
+cudaError_t launch_paged_write(const WriteArgs& a, cudaStream_t stream);
+
+struct PagedAttnArgs {
+  const void* q;                // [T, Hq, d], q_stride elements between tokens
+  const void* k_cache;          // [num_blocks, block_size, Hkv, d]
+  const void* v_cache;
+  const int32_t* block_tables;  // [N, max_blocks]
+  const int32_t* seq_lens;      // [N]
+  const int32_t* cu_seqlens;    // [N + 1]
+  void* out;                    // [T, Hq, d]
+  float* lse;                   // [T, Hq] or null
+  void* workspace;
+  long long q_stride;
+  int N, T, Hq, Hkv, d, max_blocks, num_blocks, block_size;
+  int max_q_len, window;
+  float scale;
+  int bf16;
+};
+size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_len);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+
+struct StepArgs {
+  const void* q;                // [T, Hk, dk]
+  const void* k;
+  const void* v;                // [T, H, dv]
+  const float* log_alpha;       // [T, H]
+  const float* beta;
+  float* pool;                  // [slots, H, dv, dk]
+  const int32_t* state_index;   // [N]
+  const int32_t* cu_seqlens;    // [N + 1]
+  const int32_t* context_lens;  // [N] or null
+  void* out;                    // [T, H, dv]
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  int N, T, Hk, H, dk, dv, slots;
+  int bf16;
+};
+cudaError_t launch_pool_step(const StepArgs& a, cudaStream_t stream);
+
+// SMs of the current device.
+int sm_count();
+
 // Reads and clears the tcgen05 kernel's device status word (synchronous copy).
 // Returns 0 if clear, else the code a bounded wait recorded.
 int tc_read_and_clear_status(cudaStream_t stream, cudaError_t* err);

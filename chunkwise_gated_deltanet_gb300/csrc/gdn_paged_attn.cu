@@ -1,0 +1,280 @@
+// Attention of each request's new tokens over its paged key/value cache, on the CUDA cores
+// in fp32 (every dtype and head size), and the kernel that joins partial results.
+//
+//     x_ij = scale q_i . k_j  for j <= pos_i (and j > pos_i - window),
+//     o_i = sum_j 2^{x'_ij - m_i} v_j / l_i,  l_i = sum_j 2^{x'_ij - m_i},
+//     lse_i = ln 2 (m_i + log2 l_i)           (x' = x log2 e, m_i the row's maximum)
+//
+// in one pass over the tiles with a running maximum m and sum l.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "paged_attn.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBN = 64;
+
+template <int D, int M>
+constexpr int simt_smem() {
+  return (M * D + kBN * (D + 4) + kBN * D + M * (kBN + 4)) * 4 + (kSchedMax + 1 + 8) * 8 + 8;
+}
+
+// Four consecutive elements as fp32.
+template <bool BF16>
+__device__ __forceinline__ float4 ld4f(const void* p, size_t i) {
+  if (BF16) {
+    const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p) + i);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  }
+  return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+}
+
+// A unit of M rows against tiles of 64 cached tokens.  16 lanes share M / 16 rows: in the
+// score product each lane has 4 keys (16 apart), in the value product D / 16 columns.  K
+// rows are padded by 4 floats so that the lanes' float4 reads fall into different banks.
+template <int D, int M, bool BF16>
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) {
+  constexpr int R = M / 16;                   // rows a thread
+  constexpr int NC = D / 16;                  // output columns a thread
+  constexpr int CV = NC >= 4 ? 4 : NC;        // of them, consecutive
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* qs = reinterpret_cast<float*>(smem);  // [M][D], scaled to log2 units
+  float* ks = qs + M * D;                      // [64][D + 4]
+  float* vs = ks + kBN * (D + 4);              // [64][D]
+  float* ps = vs + kBN * D;                    // [M][64 + 4]
+  long long* pre = reinterpret_cast<long long*>(ps + M * (kBN + 4));
+  long long* wsum = pre + kSchedMax + 1;
+
+  Sched<M, kBN> sched;
+  sched.template init<kThreads>(a.s, pre, wsum, blockIdx.x, gridDim.x);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  Item it;
+  while (sched.next(&it)) {
+    const int g = a.s.g, row0 = it.blk * M;
+    const int past = it.r.kl - it.r.ql;  // position of the request's first new token
+    __syncthreads();
+    for (int e = tid; e < M * D / 4; e += kThreads) {
+      const int rr = e / (D / 4), c = (e - rr * (D / 4)) * 4, row = row0 + rr;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < it.r.rows) {
+        const int tok = it.r.q0 + row / g, head = it.h * g + row % g;
+        x = ld4f<BF16>(a.q, (size_t)tok * a.q_stride + (size_t)head * D + c);
+      }
+      *reinterpret_cast<float4*>(qs + rr * D + c) =
+          make_float4(x.x * a.scale_log2, x.y * a.scale_log2, x.z * a.scale_log2, x.w * a.scale_log2);
+    }
+    int pos[R];
+    float m[R], l[R], o[R][NC];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int row = row0 + ty * R + i;
+      pos[i] = row < it.r.rows ? past + row / g : -1;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+    }
+    const int pos_first = past + row0 / g;
+    const int pos_last = past + (min(it.r.rows, row0 + M) - 1) / g;
+    const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
+
+    for (int t = it.tb; t < it.te; ++t) {
+      __syncthreads();
+      for (int e = tid; e < kBN * D / 4; e += kThreads) {
+        const int jj = e / (D / 4), c = (e - jj * (D / 4)) * 4, j = t * kBN + jj;
+        float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
+        if (j < it.r.kl) {
+          const int id = __ldg(table + j / a.bs);
+          if (id >= 0 && id < a.num_blocks) {
+            const size_t at = (((size_t)id * a.bs + j % a.bs) * a.s.Hkv + it.h) * D + c;
+            kk = ld4f<BF16>(a.kc, at);
+            vv = ld4f<BF16>(a.vc, at);
+          }
+        }
+        *reinterpret_cast<float4*>(ks + jj * (D + 4) + c) = kk;
+        *reinterpret_cast<float4*>(vs + jj * D + c) = vv;
+      }
+      __syncthreads();
+      float x[R][4];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[i][c] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 kk[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          kk[c] = *reinterpret_cast<const float4*>(ks + (tx + 16 * c) * (D + 4) + d);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float4 qq = *reinterpret_cast<const float4*>(qs + (ty * R + i) * D + d);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            x[i][c] = fmaf(qq.x, kk[c].x, x[i][c]);
+            x[i][c] = fmaf(qq.y, kk[c].y, x[i][c]);
+            x[i][c] = fmaf(qq.z, kk[c].z, x[i][c]);
+            x[i][c] = fmaf(qq.w, kk[c].w, x[i][c]);
+          }
+        }
+      }
+      const bool edge = t * kBN + kBN - 1 > pos_first ||
+                        (a.s.window > 0 && t * kBN <= pos_last - a.s.window);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float mx = m[i];
+        if (edge || pos[i] < 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int j = t * kBN + tx + 16 * c;
+            const bool seen = j <= pos[i] && (a.s.window <= 0 || j > pos[i] - a.s.window);
+            x[i][c] = seen ? x[i][c] : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx = fmaxf(mx, x[i][c]);
+#pragma unroll
+        for (int q = 8; q > 0; q >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+        const float safe = mx == -INFINITY ? 0.f : mx;
+        const float fade = exp2f(m[i] - safe);
+        m[i] = mx;
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float p = exp2f(x[i][c] - safe);
+          sum += p;
+          ps[(ty * R + i) * (kBN + 4) + tx + 16 * c] = p;
+        }
+#pragma unroll
+        for (int q = 8; q > 0; q >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+        l[i] = l[i] * fade + sum;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[i][c] *= fade;
+      }
+      __syncwarp();  // a row's probabilities come from the 16 lanes that read them
+      for (int j = 0; j < kBN; j += 4) {
+        float4 pp[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          pp[i] = *reinterpret_cast<const float4*>(ps + (ty * R + i) * (kBN + 4) + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float vv[NC];
+#pragma unroll
+          for (int b = 0; b < NC / CV; ++b)
+#pragma unroll
+            for (int c = 0; c < CV; ++c) vv[b * CV + c] = vs[(j + u) * D + b * 16 * CV + tx * CV + c];
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float p = u == 0 ? pp[i].x : u == 1 ? pp[i].y : u == 2 ? pp[i].z : pp[i].w;
+            // a token that the row does not see adds nothing, not even 0 * inf
+            if (!edge || p != 0.f) {
+#pragma unroll
+              for (int c = 0; c < NC; ++c) o[i][c] = fmaf(p, vv[c], o[i][c]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int rr = ty * R + i, row = row0 + rr;
+      if (row >= it.r.rows) continue;
+      const int tok = it.r.q0 + row / g, head = it.h * g + row % g;
+      if (it.whole) {
+        const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+        const size_t at = ((size_t)tok * a.Hq + head);
+        if (a.lse && tx == 0) a.lse[at] = lse_of(m[i], l[i]);
+#pragma unroll
+        for (int b = 0; b < NC / CV; ++b)
+#pragma unroll
+          for (int c = 0; c < CV; ++c)
+            st_out<BF16>(a.out, at * D + b * 16 * CV + tx * CV + c, o[i][b * CV + c] * inv);
+      } else {
+        const size_t at = (size_t)it.slot * M + rr;
+        if (tx == 0) a.part_ml[at] = make_float2(m[i], l[i]);
+#pragma unroll
+        for (int b = 0; b < NC / CV; ++b)
+#pragma unroll
+          for (int c = 0; c < CV; ++c)
+            a.part_o[at * D + b * 16 * CV + tx * CV + c] = o[i][b * CV + c];
+      }
+    }
+  }
+}
+
+template <int D, int M>
+cudaError_t launch_simt(const AttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
+  constexpr int bytes = simt_smem<D, M>();
+  cudaError_t e;
+  if (bf16) {
+    static std::atomic<unsigned long long> done{0};
+    e = ensure_smem_cap(paged_simt_kernel<D, M, true>, bytes, done);
+    if (e != cudaSuccess) return e;
+    paged_simt_kernel<D, M, true><<<grid, kThreads, bytes, stream>>>(a);
+  } else {
+    static std::atomic<unsigned long long> done{0};
+    e = ensure_smem_cap(paged_simt_kernel<D, M, false>, bytes, done);
+    if (e != cudaSuccess) return e;
+    paged_simt_kernel<D, M, false><<<grid, kThreads, bytes, stream>>>(a);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_combine<D, M, kBN>(a, bf16, grid, stream);
+}
+
+template <int M>
+cudaError_t launch_simt_d(const AttnArgs& a, int d, bool bf16, int grid, cudaStream_t stream) {
+  switch (d) {
+    case 16: return launch_simt<16, M>(a, bf16, grid, stream);
+    case 32: return launch_simt<32, M>(a, bf16, grid, stream);
+    case 64: return launch_simt<64, M>(a, bf16, grid, stream);
+    case 128: return launch_simt<128, M>(a, bf16, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+int simt_grid() { return sm_count(); }
+
+size_t part_bytes(int grid, int M, int d) { return (size_t)2 * grid * M * (d + 2) * 4; }
+
+}  // namespace
+
+size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_len) {
+  const long long rows = (long long)max_q_len * (Hq / Hkv);
+  return part_bytes(simt_grid(), rows <= 16 ? 16 : 64, d);
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
+  if (a.T == 0) return cudaSuccess;
+  const long long rows = (long long)a.max_q_len * (a.Hq / a.Hkv);
+  AttnArgs k{};
+  k.q = a.q; k.kc = a.k_cache; k.vc = a.v_cache; k.out = a.out; k.lse = a.lse;
+  k.q_stride = a.q_stride; k.Hq = a.Hq; k.bs = a.block_size; k.num_blocks = a.num_blocks;
+  k.scale_log2 = a.scale * 1.4426950408889634f;
+  k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.Hkv = a.Hkv; k.s.window = a.window;
+  k.s.max_blocks = a.max_blocks; k.s.max_kv = (long long)a.max_blocks * a.block_size;
+  k.s.rows_lo = 0; k.s.rows_hi = 0x7fffffff; k.s.min_tiles = 1;
+  const int grid = simt_grid(), M = rows <= 16 ? 16 : 64;
+  k.part_o = reinterpret_cast<float*>(a.workspace);
+  k.part_ml = reinterpret_cast<float2*>(k.part_o + (size_t)2 * grid * M * a.d);
+  for (int n0 = 0; n0 < a.N; n0 += kSchedMax) {
+    k.s.nn = a.N - n0 < kSchedMax ? a.N - n0 : kSchedMax;
+    k.s.seq_lens = a.seq_lens + n0;
+    k.s.cu_seqlens = a.cu_seqlens + n0;
+    k.s.block_tables = a.block_tables + (size_t)n0 * a.max_blocks;
+    const cudaError_t e = M == 16 ? launch_simt_d<16>(k, a.d, a.bf16, grid, stream)
+                                  : launch_simt_d<64>(k, a.d, a.bf16, grid, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace gdn

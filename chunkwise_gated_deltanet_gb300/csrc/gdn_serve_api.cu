@@ -1,0 +1,219 @@
+// C ABI of the serving operators: argument checks and error reporting.  The operations and
+// the meaning of every argument are documented in include/gdn.h.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/gdn.h"
+#include "gdn_internal.h"
+
+namespace {
+
+using gdn::set_error;
+
+bool head_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool dtype_ok(int t) { return t == GDN_F32 || t == GDN_BF16; }
+int elem_size(int t) { return t == GDN_BF16 ? 2 : 4; }
+
+struct Ptr {
+  const void* p;
+  const char* name;
+};
+// Non-NULL and `align`-byte aligned, or GDN_EINVAL with a message.
+int check_ptrs(const char* fn, const Ptr* ps, int n, unsigned align) {
+  for (int i = 0; i < n; ++i) {
+    if (!ps[i].p) return set_error(GDN_EINVAL, "%s: %s must be non-NULL", fn, ps[i].name);
+    if ((uintptr_t)ps[i].p % align)
+      return set_error(GDN_EINVAL, "%s: %s is not %u-byte aligned", fn, ps[i].name, align);
+  }
+  return GDN_OK;
+}
+// Elements between tokens: at least a token's own, rows 16-byte aligned, in range.
+int check_stride(const char* fn, const char* name, long long stride, long long row, int esz) {
+  if (stride < row || stride * esz % 16 || stride > (1LL << 40))
+    return set_error(GDN_EINVAL,
+                     "%s: %s must be at least %lld elements and a multiple of 16 bytes (got %lld)",
+                     fn, name, row, stride);
+  return GDN_OK;
+}
+int check_blocks(const char* fn, int num_blocks, int block_size) {
+  if (num_blocks <= 0 || block_size <= 0 || block_size % 8 || block_size > 1024)
+    return set_error(GDN_EINVAL,
+                     "%s: need num_blocks > 0 and block_size a multiple of 8 up to 1024 (got %d, %d)",
+                     fn, num_blocks, block_size);
+  if ((long long)num_blocks * block_size > 0x7fffffffLL)
+    return set_error(GDN_EINVAL, "%s: num_blocks * block_size must be below 2^31", fn);
+  return GDN_OK;
+}
+int launched(const char* fn, cudaError_t e) {
+  if (e != cudaSuccess)
+    return set_error(GDN_ELAUNCH, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_paged_plan(const int32_t* context_lens, const int32_t* new_lens, int32_t* block_tables,
+                   int32_t* free_ring, const int32_t* ring_in, int32_t* ring_out,
+                   int32_t* cu_seqlens, int32_t* seq_lens, int32_t* slot_map, int32_t* positions,
+                   int32_t* granted, int N, int T, int max_blocks, int num_blocks, int block_size,
+                   void* stream) {
+  const char* fn = "gdn_paged_plan";
+  if (N < 0 || T < 0 || max_blocks <= 0)
+    return set_error(GDN_EINVAL, "%s: need N, T >= 0 and max_blocks > 0 (got %d, %d, %d)", fn, N, T,
+                     max_blocks);
+  if (int st = check_blocks(fn, num_blocks, block_size)) return st;
+  if ((long long)max_blocks * block_size > 0x7fffffffLL - 1024 ||
+      (long long)N * max_blocks > 0x7fffffffLL)
+    return set_error(GDN_EINVAL, "%s: block_tables too large (N * max_blocks, or max_blocks * "
+                     "block_size, passes 2^31)", fn);
+  const Ptr need[] = {{free_ring, "free_ring"}, {ring_in, "ring_in"}, {ring_out, "ring_out"},
+                      {cu_seqlens, "cu_seqlens"}};
+  if (int st = check_ptrs(fn, need, 4, 4)) return st;
+  const Ptr per_req[] = {{context_lens, "context_lens"}, {new_lens, "new_lens"},
+                         {block_tables, "block_tables"}, {seq_lens, "seq_lens"},
+                         {granted, "granted"}};
+  if (N > 0)
+    if (int st = check_ptrs(fn, per_req, 5, 4)) return st;
+  const Ptr per_tok[] = {{slot_map, "slot_map"}, {positions, "positions"}};
+  if (T > 0)
+    if (int st = check_ptrs(fn, per_tok, 2, 4)) return st;
+  if (ring_in == ring_out)
+    return set_error(GDN_EINVAL, "%s: ring_out must not be ring_in", fn);
+  gdn::PlanArgs a;
+  a.context_lens = context_lens; a.new_lens = new_lens; a.block_tables = block_tables;
+  a.free_ring = free_ring; a.ring_in = ring_in; a.ring_out = ring_out; a.cu_seqlens = cu_seqlens;
+  a.seq_lens = seq_lens; a.slot_map = slot_map; a.positions = positions; a.granted = granted;
+  a.N = N; a.T = T; a.max_blocks = max_blocks; a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  return launched(fn, gdn::launch_paged_plan(a, (cudaStream_t)stream));
+}
+
+int gdn_paged_write(const void* k, const void* v, const int32_t* slot_map, void* k_cache,
+                    void* v_cache, int T, int Hkv, int d, int num_blocks, int block_size,
+                    long long k_stride, long long v_stride, int kv_dtype, void* stream) {
+  const char* fn = "gdn_paged_write";
+  if (!dtype_ok(kv_dtype))
+    return set_error(GDN_EDTYPE, "%s: kv_dtype %d is neither GDN_F32 nor GDN_BF16", fn, kv_dtype);
+  if (T < 0 || Hkv <= 0 || Hkv > (1 << 20) || !head_ok(d))
+    return set_error(GDN_EINVAL, "%s: need T >= 0, Hkv > 0 and d 16, 32, 64 or 128 (got %d, %d, %d)",
+                     fn, T, Hkv, d);
+  if (int st = check_blocks(fn, num_blocks, block_size)) return st;
+  if (T == 0) return GDN_OK;
+  const int esz = elem_size(kv_dtype);
+  const long long row = (long long)Hkv * d;
+  const Ptr big[] = {{k, "k"}, {v, "v"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}};
+  if (int st = check_ptrs(fn, big, 4, 16)) return st;
+  const Ptr map[] = {{slot_map, "slot_map"}};
+  if (int st = check_ptrs(fn, map, 1, 4)) return st;
+  if (int st = check_stride(fn, "k_stride", k_stride, row, esz)) return st;
+  if (int st = check_stride(fn, "v_stride", v_stride, row, esz)) return st;
+  gdn::WriteArgs a;
+  a.k = k; a.v = v; a.slot_map = slot_map; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_stride = k_stride * esz; a.v_stride = v_stride * esz;
+  a.T = T; a.row_bytes = (int)(row * esz);
+  a.slots = (long long)num_blocks * block_size;
+  return launched(fn, gdn::launch_paged_write(a, (cudaStream_t)stream));
+}
+
+size_t gdn_paged_attention_workspace_bytes(int Hq, int Hkv, int d, int max_q_len, int qkv_dtype) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || !head_ok(d) || max_q_len < 0 || !dtype_ok(qkv_dtype))
+    return 0;
+  return gdn::paged_attn_workspace_bytes(Hq, Hkv, d, qkv_dtype == GDN_BF16, max_q_len);
+}
+
+int gdn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, const int32_t* seq_lens,
+                        const int32_t* cu_seqlens, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int N, int T, int Hq, int Hkv, int d,
+                        int max_blocks, int num_blocks, int block_size, int max_q_len,
+                        int max_seq_len, int window, float scale, long long q_stride,
+                        int qkv_dtype, void* stream) {
+  const char* fn = "gdn_paged_attention";
+  if (!dtype_ok(qkv_dtype))
+    return set_error(GDN_EDTYPE, "%s: qkv_dtype %d is neither GDN_F32 nor GDN_BF16", fn, qkv_dtype);
+  if (N < 0 || T < 0)
+    return set_error(GDN_EINVAL, "%s: need N, T >= 0 (got %d, %d)", fn, N, T);
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv)
+    return set_error(GDN_EINVAL, "%s: Hq must be a positive multiple of Hkv (got %d, %d)", fn, Hq,
+                     Hkv);
+  if (!head_ok(d))
+    return set_error(GDN_EINVAL, "%s: d must be 16, 32, 64 or 128 (got %d)", fn, d);
+  if (int st = check_blocks(fn, num_blocks, block_size)) return st;
+  if (max_blocks <= 0 || (long long)max_blocks * block_size > 0x7fffffffLL - 1024)
+    return set_error(GDN_EINVAL, "%s: need max_blocks > 0 with max_blocks * block_size below 2^31 "
+                     "(got %d)", fn, max_blocks);
+  if (max_q_len < 0 || max_seq_len < 0 || window < 0)
+    return set_error(GDN_EINVAL, "%s: max_q_len, max_seq_len and window must be >= 0", fn);
+  if (!(scale > 0.f) || !isfinite(scale))
+    return set_error(GDN_EINVAL, "%s: scale must be positive and finite", fn);
+  if ((long long)T * Hq > 0x7fffffffLL)
+    return set_error(GDN_EINVAL, "%s: problem too large (T * Hq passes 2^31)", fn);
+  if (N == 0 || T == 0) return GDN_OK;
+  const Ptr big[] = {{q, "q"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}, {out, "out"},
+                     {workspace, "workspace"}};
+  if (int st = check_ptrs(fn, big, 5, 16)) return st;
+  const Ptr maps[] = {{block_tables, "block_tables"}, {seq_lens, "seq_lens"},
+                      {cu_seqlens, "cu_seqlens"}};
+  if (int st = check_ptrs(fn, maps, 3, 4)) return st;
+  if (lse && (uintptr_t)lse % 4)
+    return set_error(GDN_EINVAL, "%s: lse is not 4-byte aligned", fn);
+  if (int st = check_stride(fn, "q_stride", q_stride, (long long)Hq * d, elem_size(qkv_dtype)))
+    return st;
+  const size_t want = gdn_paged_attention_workspace_bytes(Hq, Hkv, d, max_q_len, qkv_dtype);
+  if (workspace_bytes < want)
+    return set_error(GDN_EINVAL, "%s: workspace holds %zu bytes, %zu are needed", fn,
+                     workspace_bytes, want);
+  gdn::PagedAttnArgs a;
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.block_tables = block_tables;
+  a.seq_lens = seq_lens; a.cu_seqlens = cu_seqlens; a.out = out; a.lse = lse;
+  a.workspace = workspace; a.q_stride = q_stride;
+  a.N = N; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.d = d;
+  a.max_blocks = max_blocks; a.num_blocks = num_blocks; a.block_size = block_size;
+  a.max_q_len = max_q_len; a.window = window; a.scale = scale;
+  a.bf16 = qkv_dtype == GDN_BF16;
+  (void)max_seq_len;
+  return launched(fn, gdn::launch_paged_attn(a, (cudaStream_t)stream));
+}
+
+int gdn_recurrent_step(const void* q, const void* k, const void* v, const float* log_alpha,
+                       const float* beta, float* state_pool, const int32_t* state_index,
+                       const int32_t* cu_seqlens, const int32_t* context_lens, void* out, int N,
+                       int T, int Hk, int H, int dk, int dv, int slots, long long q_stride,
+                       long long k_stride, long long v_stride, int qkv_dtype, void* stream) {
+  const char* fn = "gdn_recurrent_step";
+  if (!dtype_ok(qkv_dtype))
+    return set_error(GDN_EDTYPE, "%s: qkv_dtype %d is neither GDN_F32 nor GDN_BF16", fn, qkv_dtype);
+  if (N < 0 || T < 0 || slots <= 0)
+    return set_error(GDN_EINVAL, "%s: need N, T >= 0 and slots > 0 (got %d, %d, %d)", fn, N, T,
+                     slots);
+  if (Hk <= 0 || H <= 0 || H % Hk)
+    return set_error(GDN_EINVAL, "%s: H must be a positive multiple of Hk (got %d, %d)", fn, H, Hk);
+  if (!head_ok(dk) || !head_ok(dv))
+    return set_error(GDN_EINVAL, "%s: dk and dv must be 16, 32, 64 or 128 (got %d, %d)", fn, dk, dv);
+  if (N == 0 || T == 0) return GDN_OK;
+  const Ptr big[] = {{q, "q"}, {k, "k"}, {v, "v"}, {state_pool, "state_pool"}, {out, "out"}};
+  if (int st = check_ptrs(fn, big, 5, 16)) return st;
+  const Ptr maps[] = {{log_alpha, "log_alpha"}, {beta, "beta"}, {state_index, "state_index"},
+                      {cu_seqlens, "cu_seqlens"}};
+  if (int st = check_ptrs(fn, maps, 4, 4)) return st;
+  if (context_lens && (uintptr_t)context_lens % 4)
+    return set_error(GDN_EINVAL, "%s: context_lens is not 4-byte aligned", fn);
+  const int esz = elem_size(qkv_dtype);
+  if (int st = check_stride(fn, "q_stride", q_stride, (long long)Hk * dk, esz)) return st;
+  if (int st = check_stride(fn, "k_stride", k_stride, (long long)Hk * dk, esz)) return st;
+  if (int st = check_stride(fn, "v_stride", v_stride, (long long)H * dv, esz)) return st;
+  if ((long long)N * H * ((dv + 15) / 16) > 0x7fffffffLL)
+    return set_error(GDN_EINVAL, "%s: problem too large", fn);
+  gdn::StepArgs a;
+  a.q = q; a.k = k; a.v = v; a.log_alpha = log_alpha; a.beta = beta; a.pool = state_pool;
+  a.state_index = state_index; a.cu_seqlens = cu_seqlens; a.context_lens = context_lens;
+  a.out = out; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.N = N; a.T = T; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv; a.slots = slots;
+  a.bf16 = qkv_dtype == GDN_BF16;
+  return launched(fn, gdn::launch_pool_step(a, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -26,7 +26,9 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_host", "gdn_chunk_fwd_host_workspace_
            "gdn_chunk_bwd", "gdn_chunk_bwd_ex", "gdn_chunk_bwd_workspace_bytes", "gdn_bwd_select_path",
            "gdn_linear_chunk_fwd", "gdn_decode_step", "gdn_state_fold", "gdn_select_path", "gdn_launches_per_call",
            "gdn_check_status", "gdn_selftest_wait_timeout", "gdn_last_error", "gdn_version",
-           "gdn_chunk_bwd_noalloc", "gdn_chunk_bwd_noalloc_max_scratch_bytes")
+           "gdn_chunk_bwd_noalloc", "gdn_chunk_bwd_noalloc_max_scratch_bytes",
+           "gdn_paged_plan", "gdn_paged_write", "gdn_paged_attention",
+           "gdn_paged_attention_workspace_bytes", "gdn_recurrent_step")
 
 
 class GdnError(RuntimeError):
@@ -86,6 +88,17 @@ def load_library(path: str = LIB_PATH):
     lib.gdn_linear_state_correct_supported.restype = I
     lib.gdn_linear_segment_map.argtypes = [P, P, I, I, I, I, P, I, P]
     lib.gdn_linear_segment_map.restype = I
+    L, F = ctypes.c_longlong, ctypes.c_float
+    lib.gdn_paged_plan.argtypes = [P] * 11 + [I] * 5 + [P]
+    lib.gdn_paged_plan.restype = I
+    lib.gdn_paged_write.argtypes = [P] * 5 + [I] * 5 + [L, L, I, P]
+    lib.gdn_paged_write.restype = I
+    lib.gdn_paged_attention.argtypes = [P] * 9 + [Z] + [I] * 11 + [F, L, I, P]
+    lib.gdn_paged_attention.restype = I
+    lib.gdn_paged_attention_workspace_bytes.argtypes = [I] * 5
+    lib.gdn_paged_attention_workspace_bytes.restype = Z
+    lib.gdn_recurrent_step.argtypes = [P] * 10 + [I] * 7 + [L, L, L, I, P]
+    lib.gdn_recurrent_step.restype = I
     for name in ("gdn_select_path", "gdn_launches_per_call"):
         getattr(lib, name).argtypes = [I, I, I, I]
         getattr(lib, name).restype = I

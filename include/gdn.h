@@ -418,6 +418,141 @@ int gdn_linear_segment_map(const float* log_alpha, float* M, int B, int H, int T
                            const int32_t* cu_seqlens, int N_seqs, void* stream);
 
 /*
+ * ------------------------------------------------------------------ serving ----------
+ *
+ * A stack that interleaves these layers with attention layers is served with two caches
+ * for its requests: a state per request for the recurrence, kept in a pool and named by
+ * an index, and pages of keys and values for attention, named by a block table.  A step
+ * adds some new tokens to each of N requests (one token while decoding, several when
+ * tokens are drafted, a chunk of a prompt), packed one request after the other.
+ *
+ *   gdn_paged_plan       block tables, slots and offsets of the step, from the lengths
+ *   gdn_paged_write      the step's keys and values into the pages
+ *   gdn_paged_attention  attention of the step's tokens over the pages
+ *   gdn_recurrent_step   the gated delta rule over the step's tokens, on the state pool
+ *
+ * The lengths stay on the device, so that one captured graph serves steps of different
+ * lengths.  The pages have no counterpart of these calls.  int32, float (lse, log_alpha,
+ * beta) arrays need their natural alignment only; the rest as stated at the top.
+ */
+
+/*
+ * gdn_paged_plan -- block tables, slots and offsets of one step, in one launch.
+ *
+ * Request n has context_lens[n] tokens in ceil(context_lens[n] / block_size) blocks, the
+ * first entries of its row of block_tables, and gets new_lens[n] tokens.  Blocks that it
+ * lacks for them come from the free ring in request order; new_lens[n] < 0 says that the
+ * request has ended, and its blocks go to the end of the ring (they can be given out by
+ * the next call, not by this one).  A request is granted if its tokens fit a row of
+ * block_tables and it needs no block, or the blocks that it and all requests before it
+ * need are free.  One that is not granted takes none; its tokens keep their rows, with
+ * slot -1 and sequence length 0, which gdn_paged_write and gdn_paged_attention pass over.
+ *
+ * context_lens, new_lens [N]             tokens held (below 0: 0), tokens added
+ * block_tables [N, max_blocks]           in place: the new blocks are entered
+ * free_ring    [num_blocks]              in place: a ring of free block numbers
+ * ring_in, ring_out [2]                  first free entry and number of free entries before
+ *                                        and after; ring_out must not be ring_in
+ * cu_seqlens   [N + 1]                   written: offsets of the requests' tokens
+ * seq_lens     [N]                       written: tokens held after the step, 0 where the
+ *                                        request ended or was not granted
+ * slot_map, positions [T]                written: block * block_size + offset (-1: none) and
+ *                                        position of each token; -1 past the last request
+ * granted      [N]                       written: 1 or 0 (0 for ended requests)
+ * T is the room for tokens; offsets past it are not written to slot_map and positions.
+ * block_size: a multiple of 8 up to 1024; num_blocks * block_size < 2^31.
+ *
+ * A block belongs to one request (blocks shared between requests are not counted).  The
+ * call can be repeated with the same inputs, and writes the same again.  Values out of
+ * range (block numbers, ring state) give slots of -1 or wrong numbers, never accesses out
+ * of bounds.  Asynchronous; errors: GDN_EINVAL before any launch, GDN_ELAUNCH.
+ */
+int gdn_paged_plan(const int32_t* context_lens, const int32_t* new_lens, int32_t* block_tables,
+                   int32_t* free_ring, const int32_t* ring_in, int32_t* ring_out,
+                   int32_t* cu_seqlens, int32_t* seq_lens, int32_t* slot_map, int32_t* positions,
+                   int32_t* granted, int N, int T, int max_blocks, int num_blocks, int block_size,
+                   void* stream);
+
+/*
+ * gdn_paged_write -- cache[slot_map[t]] = row t for keys and values, in one launch.
+ *
+ * k, v       [T, Hkv, d] kv_dtype, k_stride / v_stride elements from token to token (at
+ *            least Hkv * d, a multiple of 16 bytes): slices of a fused projection will do
+ * slot_map   [T] block * block_size + offset; a slot out of range is passed over
+ * k_cache, v_cache [num_blocks, block_size, Hkv, d] kv_dtype; no overlap with k and v
+ * Two tokens with one slot leave either's row.  Asynchronous; errors as gdn_paged_plan,
+ * and GDN_EDTYPE.
+ */
+int gdn_paged_write(const void* k, const void* v, const int32_t* slot_map, void* k_cache,
+                    void* v_cache, int T, int Hkv, int d, int num_blocks, int block_size,
+                    long long k_stride, long long v_stride, int kv_dtype, void* stream);
+
+/*
+ * gdn_paged_attention -- softmax attention of each request's new tokens over its pages,
+ * which hold the new tokens too (gdn_paged_write first):
+ *
+ *     x_ij = scale q_i . k_j,   o_i = sum_j softmax_j(x_ij) v_j,   lse_i = log sum_j e^{x_ij}
+ *
+ * over the tokens j <= pos_i (and j > pos_i - window where window > 0), where the last of
+ * a request's new tokens has position seq_lens[n] - 1.  A token that sees nothing (a
+ * sequence shorter than its new tokens, or of length 0) gets o = 0 and lse = -inf.  What
+ * pages hold past a sequence's end is not used, whatever it is.
+ *
+ * q          [T, Hq, d] qkv_dtype, q_stride elements from token to token (at least Hq * d,
+ *            a multiple of 16 bytes); query head h reads key/value head h / (Hq / Hkv)
+ * k_cache, v_cache [num_blocks, block_size, Hkv, d] qkv_dtype
+ * block_tables [N, max_blocks]; an entry out of range reads as a block of zeros
+ * seq_lens   [N] tokens in the pages after the step (clamped to the table's room)
+ * cu_seqlens [N + 1] offsets of the requests' new tokens in q (clamped to [0, T])
+ * out        [T, Hq, d] qkv_dtype, and lse [T, Hq] fp32 or NULL: written for every token of
+ *            every request, not for rows outside all of them
+ * workspace  device scratch of gdn_paged_attention_workspace_bytes(...) bytes, no
+ *            initialisation needed; calls that overlap on the GPU need one each
+ * max_q_len  the most new tokens of a request (a larger value costs speed only)
+ * max_seq_len the most tokens of a sequence, 0 if not known (for speed only)
+ * scale      positive
+ *
+ * Scores, softmax and sums are fp32; out is rounded once.  Deterministic.  Asynchronous;
+ * errors as gdn_paged_write, and GDN_EINVAL for a short workspace.
+ */
+int gdn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, const int32_t* seq_lens,
+                        const int32_t* cu_seqlens, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int N, int T, int Hq, int Hkv, int d,
+                        int max_blocks, int num_blocks, int block_size, int max_q_len,
+                        int max_seq_len, int window, float scale, long long q_stride,
+                        int qkv_dtype, void* stream);
+
+/* Workspace bytes gdn_paged_attention needs on the current device; 0 for invalid sizes. */
+size_t gdn_paged_attention_workspace_bytes(int Hq, int Hkv, int d, int max_q_len, int qkv_dtype);
+
+/*
+ * gdn_recurrent_step -- the recurrence of gdn_decode_step over each request's new tokens
+ * in order, on a pool of states: for request n, S = state_pool[state_index[n]] is read
+ * once, carried over tokens cu_seqlens[n] .. cu_seqlens[n + 1] and written back once.
+ *
+ * q, k       [T, Hk, dk] qkv_dtype; value head h uses key head h / (H / Hk)
+ * v          [T, H, dv] qkv_dtype
+ * q_stride, k_stride, v_stride: elements from token to token (multiples of 16 bytes)
+ * log_alpha, beta [T, H] fp32
+ * state_pool [slots, H, dv, dk] fp32, updated IN PLACE for the requests that have tokens
+ * state_index [N] slot of each request; out of range: the state is passed over and the
+ *            request's outputs are zeros.  Two requests with one slot race.
+ * cu_seqlens [N + 1] offsets of the requests' tokens (clamped to [0, T])
+ * context_lens [N] or NULL: where it is 0 the request is new and starts from a zero state,
+ *            whatever its slot holds; a new request without tokens leaves its slot as it is
+ * out        [T, H, dv] qkv_dtype, written for every token of every request
+ *
+ * fp32 arithmetic on the CUDA cores, token by token: meant for a token to a few dozen per
+ * request (longer prompts: gdn_chunk_fwd).  Asynchronous; errors as gdn_paged_write.
+ */
+int gdn_recurrent_step(const void* q, const void* k, const void* v, const float* log_alpha,
+                       const float* beta, float* state_pool, const int32_t* state_index,
+                       const int32_t* cu_seqlens, const int32_t* context_lens, void* out, int N,
+                       int T, int Hk, int H, int dk, int dv, int slots, long long q_stride,
+                       long long k_stride, long long v_stride, int qkv_dtype, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the device status word that kernels
  * set when a bounded wait (mbarrier, async copy) gives up.  Returns GDN_OK or
  * GDN_ETIMEOUT (message names the wait), or GDN_ECUDA if the stream failed.
