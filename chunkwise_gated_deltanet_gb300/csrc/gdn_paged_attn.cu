@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "paged_attn.cuh"
 
 namespace gdn {
@@ -20,7 +22,7 @@ constexpr int kBN = 64;
 
 template <int D, int M>
 constexpr int simt_smem() {
-  return (M * D + kBN * (D + 4) + kBN * D + M * (kBN + 4)) * 4 + (kSchedMax + 1 + 8) * 8 + 8;
+  return (M * D + kBN * (D + 4) + kBN * D + M * (kBN + 4)) * 4 + (int)sizeof(SchedMem<false>);
 }
 
 // Four consecutive elements as fp32.
@@ -47,11 +49,10 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
   float* ks = qs + M * D;                      // [64][D + 4]
   float* vs = ks + kBN * (D + 4);              // [64][D]
   float* ps = vs + kBN * D;                    // [M][64 + 4]
-  long long* pre = reinterpret_cast<long long*>(ps + M * (kBN + 4));
-  long long* wsum = pre + kSchedMax + 1;
+  auto* mem = reinterpret_cast<SchedMem<false>*>(ps + M * (kBN + 4));
 
-  Sched<M, kBN> sched;
-  sched.template init<kThreads>(a.s, pre, wsum, blockIdx.x, gridDim.x);
+  Sched<M, kBN, false> sched;
+  sched.template init<kThreads>(a.s, mem, blockIdx.x, gridDim.x);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   Item it;
   while (sched.next(&it)) {
@@ -227,7 +228,7 @@ cudaError_t launch_simt(const AttnArgs& a, bool bf16, int grid, cudaStream_t str
   }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_combine<D, M, kBN>(a, bf16, grid, stream);
+  return launch_join<D, M, kBN, false>(a, bf16, grid, stream);
 }
 
 template <int M>
@@ -247,31 +248,50 @@ size_t part_bytes(int grid, int M, int d) { return (size_t)2 * grid * M * (d + 2
 
 }  // namespace
 
+// Which kernels a call runs, from the most query rows of a request and key/value head:
+// the tensor-core kernel takes the requests with more than kShortRows rows, the CUDA-core
+// one the others and every other type and head size.
+constexpr int kShortRows = 16;
+
 size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_len) {
-  const long long rows = (long long)max_q_len * (Hq / Hkv);
-  return part_bytes(simt_grid(), rows <= 16 ? 16 : 64, d);
+  const int grid = simt_grid();
+  const bool longer = (long long)max_q_len * (Hq / Hkv) > kShortRows;
+  if (bf16 && d >= 64)
+    return std::max(part_bytes(grid, 16, d), longer ? paged_tc_part_bytes(grid, d) : 0);
+  return part_bytes(grid, longer ? 64 : 16, d);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  const long long rows = (long long)a.max_q_len * (a.Hq / a.Hkv);
+  const bool longer = (long long)a.max_q_len * (a.Hq / a.Hkv) > kShortRows;
+  const bool tc = longer && a.bf16 && a.d >= 64;
   AttnArgs k{};
   k.q = a.q; k.kc = a.k_cache; k.vc = a.v_cache; k.out = a.out; k.lse = a.lse;
   k.q_stride = a.q_stride; k.Hq = a.Hq; k.bs = a.block_size; k.num_blocks = a.num_blocks;
   k.scale_log2 = a.scale * 1.4426950408889634f;
   k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.Hkv = a.Hkv; k.s.window = a.window;
   k.s.max_blocks = a.max_blocks; k.s.max_kv = (long long)a.max_blocks * a.block_size;
-  k.s.rows_lo = 0; k.s.rows_hi = 0x7fffffff; k.s.min_tiles = 1;
-  const int grid = simt_grid(), M = rows <= 16 ? 16 : 64;
+  k.s.min_tiles = 1;
+  const int grid = simt_grid(), M = longer && !tc ? 64 : 16;
   k.part_o = reinterpret_cast<float*>(a.workspace);
-  k.part_ml = reinterpret_cast<float2*>(k.part_o + (size_t)2 * grid * M * a.d);
   for (int n0 = 0; n0 < a.N; n0 += kSchedMax) {
     k.s.nn = a.N - n0 < kSchedMax ? a.N - n0 : kSchedMax;
     k.s.seq_lens = a.seq_lens + n0;
     k.s.cu_seqlens = a.cu_seqlens + n0;
     k.s.block_tables = a.block_tables + (size_t)n0 * a.max_blocks;
-    const cudaError_t e = M == 16 ? launch_simt_d<16>(k, a.d, a.bf16, grid, stream)
-                                  : launch_simt_d<64>(k, a.d, a.bf16, grid, stream);
+    cudaError_t e = cudaSuccess;
+    if (tc) {
+      // one request: whatever its length is, so that nothing is left over
+      k.s.rows_lo = a.N > 1 ? kShortRows : 0;
+      k.s.rows_hi = 0x7fffffff;
+      if ((e = launch_paged_tc(k, a.d, grid, stream)) != cudaSuccess) return e;
+      if (a.N == 1) break;
+    }
+    k.s.rows_lo = 0;
+    k.s.rows_hi = tc ? kShortRows : 0x7fffffff;
+    k.part_ml = reinterpret_cast<float2*>(k.part_o + (size_t)2 * grid * M * a.d);
+    e = M == 16 ? launch_simt_d<16>(k, a.d, a.bf16, grid, stream)
+                : launch_simt_d<64>(k, a.d, a.bf16, grid, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

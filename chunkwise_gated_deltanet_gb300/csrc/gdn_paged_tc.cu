@@ -1,0 +1,563 @@
+// Attention of chunks of new tokens over the paged cache on the tensor cores (bf16,
+// d = 64 or 128): the score and value products with tcgen05, K and V tiles by TMA from
+// their pages.
+//
+//   S = Q K^T (fp32 in TMEM), P = 2^{sl (S - m)} (bf16, over S in TMEM), O += P V (TMEM)
+//
+// Bound by the tensor cores: 4 d operations a (row, key) pair against 2^x on the special
+// function units, which a tile's softmax needs about as long as one of its two products
+// does.  So a unit has 256 rows as two halves of 128, each with a warpgroup of its own (a
+// thread a row: no exchange for the row's maximum and sum): while one half's softmax runs,
+// the tensor cores work on the other half's products.  The halves share the K and V tiles,
+// which also halves the reads from L2.
+//
+//   warps 0-3, 4-7  softmax of the two halves: Q into shared memory, S out of TMEM, P into
+//                   it, and the output
+//   warp 8          one thread issues every MMA
+//   warp 9          schedules, looks up pages and issues the TMA loads
+//   (warps 10, 11 fill the third warpgroup, which hands registers to the other two:
+//   384 threads x 168 = 256 x 200 + 128 x 104)
+//
+// TMEM (512 columns): S_0 | S_1 | O_0 | O_1, 128 each; P_h takes the first 64 columns of
+// S_h.  S_h of the next tile is computed after P_h V of this one, in the order of issue on
+// the same pipe.  The barrier that says that it is done says so for P_h V as well, so the
+// softmax warps can rescale O after it without another wait.
+//
+// The running maximum m is raised only when a score passes it by more than 8 (in log2
+// units): P and the sums may then be up to 2^8 larger, exact in fp32 and of the same
+// relative precision in bf16, and rescaling O, a pass over TMEM, becomes rare.  P is
+// rounded to bf16 for the tensor cores; l sums the unrounded values.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <numeric>
+
+#include "paged_attn.cuh"
+#include "tc_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kTcM = 256, kTcBN = 128, kTcThreads = 384, kItems = 4;
+constexpr float kRaise = 8.f;  // log2 units by which a score may pass the running maximum
+
+struct TcItem {
+  int valid, n, h, blk, q0, ql, kl, rows, tb, te, whole, slot;
+};
+
+template <int D>
+struct TcSmem {
+  static constexpr int kPanel = 128 * 128;             // 128 rows of 64 bf16
+  static constexpr int kTile = kPanel * (D / 64);
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  uint8_t q[2][kTile];
+  uint8_t kv[kStages][kTile];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  TcItem items[kItems];
+  SchedMem<true> sched;
+  uint32_t tmem;
+  int abort_flag;
+  int bad[kItems];  // a value that some row does not see is not finite
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// wait_bar in line: a kernel that moves registers between its warpgroups has no calls.
+__device__ __forceinline__ bool wait_in(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      atomicOr((int*)abort_flag, ST_WAIT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool warp_waits(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait_in(bar, parity, abort_flag)) != 0;
+}
+
+// Whether tile `t` has tokens that some row of the unit does not see.
+__device__ __forceinline__ bool edge_tile(int t, int pos_first, int pos_last, int window) {
+  return t * kTcBN + kTcBN - 1 > pos_first || (window > 0 && t * kTcBN <= pos_last - window);
+}
+__device__ __forceinline__ bool not_finite(uint32_t two) {
+  return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
+}
+
+// Q rows of one half into its K-major tile: 16-byte pieces, rows past the unit as zeros.
+template <int D>
+__device__ void load_q(const AttnArgs& a, const TcItem& it, int half, uint8_t* tile, int wt) {
+  constexpr int CH = D / 8;  // pieces a row
+  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+  const int g = a.s.g, row0 = it.blk * kTcM + half * 128;
+#pragma unroll 1
+  for (int e0 = 0; e0 < 128 * CH; e0 += 128 * 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int e = e0 + u * 128 + wt, rr = e / CH, c = e % CH, row = row0 + rr;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (row < it.rows) {
+        const int tok = row / g, head = it.h * g + (row - tok * g);
+        x[u] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)(it.q0 + tok) * a.q_stride +
+                                                    (size_t)head * D + c * 8));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int e = e0 + u * 128 + wt, rr = e / CH, c = e % CH;
+      st_shared_v4(smem_u32(tile + sw128_offset(rr, c * 8, 128)), x[u].x, x[u].y, x[u].z, x[u].w);
+    }
+  }
+  fence_async_smem();
+}
+
+// A thread's row of one half, over all of this CTA's items.
+template <int D>
+__device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int half) {
+  const int wt = threadIdx.x & 127, lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
+  volatile int* abort_flag = &sm.abort_flag;
+  // every lane of the warp leaves together: the TMEM instructions need all of them
+  auto waits = [&](uint64_t* bar, uint32_t parity) {
+    return warp_waits(bar, parity, abort_flag);
+  };
+  const float sl = a.scale_log2;
+  const int g = a.s.g, window = a.s.window;
+  uint32_t ntile = 0, nitem = 0, kv = 0;  // tiles and items of this half; K/V loads of the CTA
+
+  if (!waits(&sm.item_full[0], 0)) return;
+  auto active = [&](const TcItem& x) {
+    return x.te > x.tb && x.rows - x.blk * kTcM > half * 128;
+  };
+  if (sm.items[0].valid && active(sm.items[0])) {
+    load_q<D>(a, sm.items[0], half, sm.q[half], wt);
+    mbar_arrive(&sm.q_full[half]);
+  }
+  for (uint32_t idx = 0;; ++idx) {
+    const TcItem& it = sm.items[idx % kItems];  // stays in shared memory: registers are S's
+    if (!it.valid) break;
+    const int past = it.kl - it.ql, row = it.blk * kTcM + half * 128 + wt;
+    const int pos_first = past + it.blk * kTcM / g;
+    const int pos_last = past + (min(it.rows, it.blk * kTcM + kTcM) - 1) / g;
+    const int pos = past + row / g;
+    const bool on = active(it);
+    float m = -INFINITY, l = 0.f;
+    if (on) {
+#pragma unroll 1
+      for (int t = it.tb, te = it.te; t < te; ++t) {
+        if (!waits(&sm.s_full[half], ntile & 1)) return;
+        ++ntile;
+        __syncwarp();
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+        tmem_wait_ld();
+        const bool edge = edge_tile(t, pos_first, pos_last, window);
+        if (edge) {
+          const int hi = pos - t * kTcBN;                            // columns seen: lo < c <= hi
+          const int lo = window > 0 ? hi - window : -1;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e > hi || 32 * c + e <= lo) s[c][e] = 0xff800000u;
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          top[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) top[c] = fmaxf(top[c], __uint_as_float(s[c][e]));
+        }
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const bool raise = (mx - m) * sl > kRaise || (m == -INFINITY && mx != -INFINITY);
+        const bool rescale = raise && m != -INFINITY;
+        float fade = 1.f;
+        if (raise) {
+          fade = ex2((m - mx) * sl);  // 0 from -inf
+          m = mx;
+          l *= fade;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {  // O of the tiles before: P V is done
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(rescale ? __uint_as_float(o[e]) * fade : __uint_as_float(o[e]));
+            tmem_st32(to + c, o);
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m * sl;
+        const uint64_t sl2 = pack2(sl, sl), off2 = pack2(off, off);
+        uint64_t sum2 = pack2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* sp = &s[2 * c + (e >> 4)][2 * (e & 15)];
+            const uint64_t x = fma2(pack2(__uint_as_float(sp[0]), __uint_as_float(sp[1])), sl2, off2);
+            float x0, x1;
+            unpack2(x, x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            sum2 = add2(sum2, pack2(x0, x1));
+            p[e] = pack_bf16(x0, x1);
+          }
+          tmem_st32(ts + 32 * c, p);
+        }
+        float s0, s1;
+        unpack2(sum2, s0, s1);
+        l += s0 + s1;
+        if (edge) {
+          // 0 * inf must not reach a row through a token that it does not see: non-finite
+          // values of this tile become zeros here and are added at the end, row by row
+          const uint32_t v = kv + 2 * (t - it.tb) + 1, slot = v % TcSmem<D>::kStages;
+          if (!waits(&sm.full[slot], (v / TcSmem<D>::kStages) & 1)) return;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(sm.kv[slot] + (c >> 3) * TcSmem<D>::kPanel + wt * 128 +
+                                                 (((c + wt) & 7) << 4));
+            const uint4 x = *at;
+            if (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w)) {
+              uint16_t* e = reinterpret_cast<uint16_t*>(at);
+              for (int i = 0; i < 8; ++i)
+                if ((e[i] & 0x7f80u) == 0x7f80u) e[i] = 0;
+              if (t * kTcBN + wt < it.kl) *reinterpret_cast<volatile int*>(&sm.bad[idx % kItems]) = 1;
+            }
+          }
+          fence_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[half]);
+      }
+    }
+    kv += 2 * (it.te - it.tb);
+
+    // the next item's Q goes in before this one's output goes out
+    const uint32_t nx = idx + 1;
+    if (!waits(&sm.item_full[nx % kItems], (nx / kItems) & 1)) return;
+    const TcItem& next = sm.items[nx % kItems];
+    if (next.valid && active(next)) {  // every score of this item is done, so Q is free
+      load_q<D>(a, next, half, sm.q[half], wt);
+      mbar_arrive(&sm.q_full[half]);
+    }
+    if (on) {
+      if (!waits(&sm.o_full[half], nitem & 1)) return;
+      ++nitem;
+      tc_fence_after();
+    }
+    const bool bad = *reinterpret_cast<volatile int*>(&sm.bad[idx % kItems]) != 0;
+    const bool mine = row < it.rows;
+    const int tok = it.q0 + row / g, head = it.h * g + row % g;
+    const size_t at = (size_t)tok * a.Hq + head;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const size_t part = (size_t)it.slot * kTcM + half * 128 + wt;
+    if (mine) {
+      if (!it.whole)
+        a.part_ml[part] = make_float2(m * sl, l);
+      else if (a.lse)
+        a.lse[at] = lse_of(m * sl, l);
+    }
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      if (on) {
+        tmem_ld32(to + c, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+      }
+      if (mine && bad) {
+        const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(a.vc);
+        const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
+        for (int t = it.tb; t < it.te; ++t) {
+          if (!edge_tile(t, pos_first, pos_last, window)) continue;
+          for (int j = t * kTcBN; j < (t + 1) * kTcBN; ++j) {
+            if (j > pos || (window > 0 && j <= pos - window)) continue;
+            const int id = __ldg(table + j / a.bs);
+            if (id < 0 || id >= a.num_blocks) continue;
+            const __nv_bfloat16* src = vc + (((size_t)id * a.bs + j % a.bs) * a.s.Hkv + it.h) * D + c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = __bfloat162float(src[e]);
+              if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+            }
+          }
+        }
+      }
+      if (mine && it.whole) {
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[8 * e + i]) * inv;
+          dst[e] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                              pack_bf16(x[6], x[7]));
+        }
+      } else if (mine) {
+        uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * D + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[idx % kItems]);
+  }
+}
+
+// One thread: every MMA of the CTA.
+template <int D>
+__device__ void run_mma(TcSmem<D>& sm, uint32_t tmem) {
+  using S = TcSmem<D>;
+  constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
+  volatile int* abort_flag = &sm.abort_flag;
+  uint32_t kv = 0, nitem[2] = {0, 0}, np[2] = {0, 0};
+  auto wait_kv = [&](uint32_t v) {
+    const bool ok = wait_in(&sm.full[v % S::kStages], (v / S::kStages) & 1, abort_flag);
+    tc_fence_after();
+    return ok;
+  };
+  auto scores = [&](uint32_t v, int half) {
+    uint64_t q = smem_desc(smem_u32(sm.q[half]), 16, 1024);
+    uint64_t k = smem_desc(smem_u32(sm.kv[v % S::kStages]), 16, 1024);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      mma_bf16(tmem + half * 128, q + (i >> 2) * (S::kPanel >> 4) + kStepK * (i & 3),
+               k + (i >> 2) * (S::kPanel >> 4) + kStepK * (i & 3), id_s, i > 0);
+    mma_commit(&sm.s_full[half]);
+  };
+  auto values = [&](uint32_t v, int half, bool first) {
+    uint64_t b = smem_desc(smem_u32(sm.kv[v % S::kStages]), S::kPanel, 1024);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      mma_bf16_ta(tmem + 256 + half * 128, tmem + half * 128 + 8 * i, b + kStepMN * i, id_o,
+                  !first || i > 0);
+  };
+  for (uint32_t idx = 0;; ++idx) {
+    if (!wait_in(&sm.item_full[idx % kItems], (idx / kItems) & 1, abort_flag)) return;
+    const TcItem& it = sm.items[idx % kItems];
+    if (!it.valid) return;
+    const int tiles = it.te - it.tb;
+    const int halves = it.rows - it.blk * kTcM > 128 ? 2 : 1;
+    mbar_arrive(&sm.item_empty[idx % kItems]);
+    if (tiles == 0) continue;
+    if (!wait_kv(kv)) return;
+    for (int h = 0; h < halves; ++h) {
+      if (!wait_in(&sm.q_full[h], nitem[h] & 1, abort_flag)) return;
+      ++nitem[h];
+      tc_fence_after();
+      scores(kv, h);
+    }
+    mma_commit(&sm.empty[kv % S::kStages]);
+    for (int j = 0; j < tiles; ++j, kv += 2) {
+      const bool more = j + 1 < tiles;
+      if (!wait_kv(kv + 1)) return;
+      if (more && !wait_kv(kv + 2)) return;
+      for (int h = 0; h < halves; ++h) {
+        if (!wait_in(&sm.p_full[h], np[h] & 1, abort_flag)) return;
+        ++np[h];
+        tc_fence_after();
+        values(kv + 1, h, j == 0);
+        if (h == halves - 1) mma_commit(&sm.empty[(kv + 1) % S::kStages]);
+        if (more)
+          scores(kv + 2, h);
+        else
+          mma_commit(&sm.o_full[h]);
+      }
+      if (more) mma_commit(&sm.empty[(kv + 2) % S::kStages]);
+    }
+  }
+}
+
+// One warp: the schedule, and the loads of K and V tiles (rows of a page at a time; pages
+// past the sequence and table entries out of range read as zeros, by a coordinate past the
+// last page).
+template <int D>
+__device__ void run_loads(TcSmem<D>& sm, const AttnArgs& a, Sched<kTcM, kTcBN, true>& sched,
+                          const CUtensorMap* mk, const CUtensorMap* mv, int box) {
+  using S = TcSmem<D>;
+  volatile int* abort_flag = &sm.abort_flag;
+  const int lane = threadIdx.x & 31;
+  const int per = kTcBN / box, boxes = per * (D / 64);  // a panel's, a tile's
+  uint32_t kv = 0;
+  for (uint32_t idx = 0;; ++idx) {
+    Item it{};
+    const bool valid = sched.next(&it);
+    if (!warp_waits(&sm.item_empty[idx % kItems], ((idx / kItems) & 1) ^ 1, abort_flag)) return;
+    if (lane == 0) {
+      sm.bad[idx % kItems] = 0;
+      sm.items[idx % kItems] = TcItem{valid, it.n, it.h, it.blk, it.r.q0, it.r.ql, it.r.kl, it.r.rows,
+                                      it.tb, it.te, it.whole, it.slot};
+      mbar_arrive(&sm.item_full[idx % kItems]);
+    }
+    if (!valid) return;
+    const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
+    auto page = [&](int t, int e) {  // of box e of tile t
+      const int j = t * kTcBN + (e % per) * box;
+      int id = -1;
+      if (e < boxes && t < it.te && j < it.r.kl) id = __ldg(table + j / a.bs);
+      return id >= 0 && id < a.num_blocks ? id : a.num_blocks;
+    };
+    int id0 = page(it.tb, lane);
+    for (int t = it.tb; t < it.te; ++t) {
+      const int next0 = page(t + 1, lane);  // in flight during this tile's waits
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w, ++kv) {
+        const uint32_t slot = kv % S::kStages;
+        if (!warp_waits(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag)) return;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
+        __syncwarp();
+        for (int e = lane; e < boxes; e += 32) {
+          const int panel = e / per, rr = (e - panel * per) * box, j = t * kTcBN + rr;
+          const int id = e == lane ? id0 : page(t, e);
+          tma_load_4d(sm.kv[slot] + panel * S::kPanel + rr * 128, w ? mv : mk, &sm.full[slot], panel * 64,
+                      it.h, j % a.bs, id);
+        }
+      }
+      id0 = next0;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv, int box, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  TcSmem<D>& sm = *reinterpret_cast<TcSmem<D>*>(
+      smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (warp == 8) tmem_alloc(&sm.tmem, 512);
+  if (tid == 0) {
+    sm.abort_flag = 0;
+    for (int i = 0; i < TcSmem<D>::kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sm.s_full[h], 1);
+      mbar_init(&sm.p_full[h], 128);
+      mbar_init(&sm.q_full[h], 128);
+      mbar_init(&sm.o_full[h], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], 9);  // eight softmax warps and the MMA thread
+    }
+    fence_mbarrier_init();
+    prefetch_tensormap(&mk);
+    prefetch_tensormap(&mv);
+  }
+  Sched<kTcM, kTcBN, true> sched;
+  sched.template init<kTcThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    run_softmax<D>(sm, a, tmem, warp >> 2);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8) {
+      if ((tid & 31) == 0) run_mma<D>(sm, tmem);
+    } else if (warp == 9) {
+      run_loads<D>(sm, a, sched, &mk, &mv, box);
+    }
+  }
+  __syncwarp();
+
+  tc_fence_before();
+  __syncthreads();
+  if (sm.abort_flag) {  // let copies and products still in flight land before TMEM goes
+    const uint64_t tw = globaltimer_ns();
+    while (globaltimer_ns() - tw < 50000ull) {
+    }
+    if (tid == 0) atomicOr(status, sm.abort_flag);
+  }
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// [num_blocks][bs][Hkv][D] bf16, boxes of 64 columns x 1 head x `box` tokens of one page.
+bool make_page_map(CUtensorMap* m, const void* base, int num_blocks, int bs, int Hkv, int D, int box_rows) {
+  auto enc = get_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)bs, (cuuint64_t)num_blocks};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)bs * Hkv * D * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_tc_d(const AttnArgs& a, int grid, cudaStream_t stream) {
+  constexpr int bytes = (int)sizeof(TcSmem<D>) + 1024;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = ensure_smem_cap(paged_tc_kernel<D>, bytes, done);
+  if (e != cudaSuccess) return e;
+  int* status = nullptr;
+  if ((e = tc_status_address(&status)) != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  const int box = std::gcd(a.bs, kTcBN);
+  if (!make_page_map(&mk, a.kc, a.num_blocks, a.bs, a.s.Hkv, D, box) ||
+      !make_page_map(&mv, a.vc, a.num_blocks, a.bs, a.s.Hkv, D, box))
+    return cudaErrorInvalidValue;
+  paged_tc_kernel<D><<<grid, kTcThreads, bytes, stream>>>(a, mk, mv, box, status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_join<D, kTcM, kTcBN, true>(a, true, grid, stream);
+}
+
+}  // namespace
+
+size_t paged_tc_part_bytes(int grid, int d) { return (size_t)2 * grid * kTcM * (d + 2) * 4; }
+
+cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream) {
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kTcM * d);
+  // whole units in waves when keys and values pass half of the L2 cache (129 MB)
+  a.s.wave_tokens = (64LL << 20) / ((long long)a.s.Hkv * d * 4);
+  return d == 128 ? launch_tc_d<128>(a, grid, stream) : launch_tc_d<64>(a, grid, stream);
+}
+
+}  // namespace gdn

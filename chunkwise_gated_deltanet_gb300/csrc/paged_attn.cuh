@@ -8,7 +8,6 @@
 #include "paged_sched.cuh"
 
 namespace gdn {
-namespace {
 
 struct AttnArgs {
   const void* q;
@@ -23,6 +22,13 @@ struct AttnArgs {
   float scale_log2;
   SchedArgs s;
 };
+
+// The tensor-core kernel for chunks of new tokens (bf16, d = 64 or 128): partial-result
+// bytes for a grid, and its launch (a.part_o set; a.part_ml is placed behind it).
+size_t paged_tc_part_bytes(int grid, int d);
+cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream);
+
+namespace {
 
 __device__ __forceinline__ float lse_of(float m, float l) {
   return m == -INFINITY ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
@@ -41,11 +47,11 @@ constexpr int kJoinRows = 8;  // rows a CTA joins, a warp each
 // Joins the partial results of the units that share boundaries cut: CTA (c - 1, y) looks
 // at the boundary between shares c - 1 and c, and if it is the first one inside its unit,
 // joins rows y * 8 .. y * 8 + 7 of it over every share that holds a part.
-template <int D, int M, int BN, bool BF16>
+template <int D, int M, int BN, bool BF16, bool WAVES>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnArgs a, int grid) {
-  __shared__ long long pre[kSchedMax + 1], wsum[kJoinThreads / 32];
-  Sched<M, BN> sched;
-  sched.template init<kJoinThreads>(a.s, pre, wsum, 0, grid);
+  __shared__ SchedMem<WAVES> mem;
+  Sched<M, BN, WAVES> sched;
+  sched.template init<kJoinThreads>(a.s, &mem, 0, grid);
   const int c = blockIdx.x + 1;
   if (c >= sched.G) return;
   const long long b = sched.share(c), before = sched.share(c - 1);
@@ -95,14 +101,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnArgs
     if (lane + 32 * j < D) st_out<BF16>(a.out, at * D + lane + 32 * j, acc[j] * inv);
 }
 
-template <int D, int M, int BN>
-cudaError_t launch_combine(const AttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
+template <int D, int M, int BN, bool WAVES>
+cudaError_t launch_join(const AttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
   if (grid < 2) return cudaSuccess;
   const dim3 g(grid - 1, M / kJoinRows);
   if (bf16)
-    paged_join_kernel<D, M, BN, true><<<g, kJoinThreads, 0, stream>>>(a, grid);
+    paged_join_kernel<D, M, BN, true, WAVES><<<g, kJoinThreads, 0, stream>>>(a, grid);
   else
-    paged_join_kernel<D, M, BN, false><<<g, kJoinThreads, 0, stream>>>(a, grid);
+    paged_join_kernel<D, M, BN, false, WAVES><<<g, kJoinThreads, 0, stream>>>(a, grid);
   return cudaGetLastError();
 }
 

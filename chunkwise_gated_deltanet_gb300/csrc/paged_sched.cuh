@@ -10,6 +10,12 @@
 // the order of the shares, so results do not depend on timing.  A share has at most two
 // partial results: the unit that its start cuts (slot 0) and the one that its end cuts
 // (slot 1).
+//
+// With WAVES, a launch whose caches do not fit L2 first gives out whole units in waves, unit
+// w * CTAs + c to CTA c (odd waves the other way round), and shares only the last one to two
+// waves as above.  The CTAs then work on neighbouring row blocks of a few heads at a time
+// and read their keys and values from L2; contiguous shares would stream every head's cache
+// from HBM at once.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -18,7 +24,6 @@
 #include "gdn_internal.h"
 
 namespace gdn {
-namespace {
 
 constexpr int kSchedMax = 1024;  // requests of one launch
 
@@ -30,7 +35,10 @@ struct SchedArgs {
   long long max_kv;           // max_blocks * block_size
   int rows_lo, rows_hi;       // requests with rows in (rows_lo, rows_hi] only
   int min_tiles;              // tiles a CTA takes at least (while there are that many)
+  long long wave_tokens;      // WAVES: cached tokens (all heads) above which waves are used
 };
+
+namespace {
 
 struct Req {
   int q0, ql, kl;
@@ -57,12 +65,22 @@ __device__ __forceinline__ Req load_req(const SchedArgs& s, int n) {
   return r;
 }
 
-template <int M, int BN>
+// Shared memory of a scheduler.
+template <bool WAVES>
+struct SchedMem {
+  long long pre[kSchedMax + 1];            // tiles before each request
+  long long warp[32];
+  int units[WAVES ? kSchedMax + 1 : 1];    // units before each request
+  int warp_u[WAVES ? 32 : 1];
+};
+
+template <int M, int BN, bool WAVES>
 struct Sched {
   SchedArgs s;
-  const long long* pre;  // tiles before each request (nn + 1 entries, shared memory)
-  long long total, first, pos, end, unit0;
+  const SchedMem<WAVES>* mem;
+  long long total, base, first, pos, end, unit0;
   int G, cta, n, h, blk;
+  int waves, wave;
   Req r;
   bool started;
 
@@ -78,16 +96,17 @@ struct Sched {
   }
   __device__ __forceinline__ static int blocks(const Req& q) { return (q.rows + M - 1) / M; }
 
-  // Whole CTA of NT threads: prefix sums of the requests' tiles into `pre_smem`.
+  // Whole CTA of NT threads: prefix sums of the requests' tiles and units into `m`.
   template <int NT>
-  __device__ void init(const SchedArgs& args, long long* pre_smem, long long* warp_smem, int cta_id,
-                       int grid) {
+  __device__ void init(const SchedArgs& args, SchedMem<WAVES>* m, int cta_id, int grid) {
     s = args;
-    pre = pre_smem;
+    mem = m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long carry = 0;
+    long long carry = 0, tokens = 0;
+    int carry_u = 0;
     for (int n0 = 0; n0 < s.nn; n0 += NT) {
       long long x = 0;
+      int u = 0;
       if (n0 + tid < s.nn) {
         const Req q = load_req(s, n0 + tid);
         const int nb = blocks(q);
@@ -95,50 +114,110 @@ struct Sched {
         bool e;
         for (int b = 0; b < nb; ++b) x += tiles(q, b, &lo, &e);
         x *= s.Hkv;
+        u = nb * s.Hkv;
+        if (WAVES && nb) tokens += q.kl;
       }
       long long inc = x;
+      int inc_u = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
+        if (WAVES) {
+          const int yu = __shfl_up_sync(0xffffffffu, inc_u, o);
+          if (lane >= o) inc_u += yu;
+        }
       }
       if (n0 > 0) __syncthreads();
-      if (lane == 31) warp_smem[warp] = inc;
-      __syncthreads();
-      long long base = carry;
-      for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) base += warp_smem[w];
-        carry += warp_smem[w];
+      if (lane == 31) {
+        m->warp[warp] = inc;
+        if (WAVES) m->warp_u[warp] = inc_u;
       }
-      if (n0 + tid < s.nn) pre_smem[n0 + tid] = base + inc - x;
+      __syncthreads();
+      long long before = carry;
+      int before_u = carry_u;
+      for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += m->warp[w];
+        carry += m->warp[w];
+        if (WAVES) {
+          if (w < warp) before_u += m->warp_u[w];
+          carry_u += m->warp_u[w];
+        }
+      }
+      if (n0 + tid < s.nn) {
+        m->pre[n0 + tid] = before + inc - x;
+        if (WAVES) m->units[n0 + tid] = before_u + inc_u - u;
+      }
     }
-    if (tid == 0) pre_smem[s.nn] = carry;
+    if (tid == 0) {
+      m->pre[s.nn] = carry;
+      if (WAVES) m->units[s.nn] = carry_u;
+    }
     __syncthreads();
     total = carry;
     const long long want = (total + s.min_tiles - 1) / s.min_tiles;
     G = (int)min((long long)grid, max(want, 1LL));
     cta = cta_id;
+    base = 0;
+    waves = 0;
+    if (WAVES) {
+      // cached tokens of the requests, over the CTA
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+      if (lane == 0) m->warp[warp] = tokens;
+      __syncthreads();
+      tokens = 0;
+      for (int w = 0; w < NT / 32; ++w) tokens += m->warp[w];
+      if (tokens > s.wave_tokens) waves = max(carry_u / G - 1, 0);
+      if (waves > 0) {
+        find_unit(waves * G);
+        base = unit0;
+      }
+    }
+    wave = 0;
     first = cta < G ? share(cta) : total;
     pos = first;
     end = cta < G ? share(cta + 1) : total;
+    if (cta >= G) waves = 0;
     started = false;
   }
-  __device__ __forceinline__ long long share(int c) const { return total * c / G; }
+  __device__ __forceinline__ long long share(int c) const { return base + (total - base) * c / G; }
 
-  // Request, head, row block and start of the unit that holds tile `x`.
-  __device__ void locate(long long x) {
+  // Request, head, row block and first tile of unit `u`.
+  __device__ void find_unit(int u) {
     int lo = 0, hi = s.nn;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= x)
+      if (mem->units[mid] <= u)
         lo = mid;
       else
         hi = mid;
     }
     n = lo;
     r = load_req(s, n);
-    const long long per = (pre[n + 1] - pre[n]) / s.Hkv;
-    long long rem = x - pre[n];
+    const int rem = u - mem->units[n], nb = blocks(r);
+    h = rem / nb;
+    blk = rem - h * nb;
+    unit0 = mem->pre[n] + (mem->pre[n + 1] - mem->pre[n]) / s.Hkv * h;
+    int l;
+    bool e;
+    for (int b = 0; b < blk; ++b) unit0 += tiles(r, b, &l, &e);
+  }
+
+  // Request, head, row block and start of the unit that holds tile `x`.
+  __device__ void locate(long long x) {
+    int lo = 0, hi = s.nn;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (mem->pre[mid] <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    n = lo;
+    r = load_req(s, n);
+    const long long per = (mem->pre[n + 1] - mem->pre[n]) / s.Hkv;
+    long long rem = x - mem->pre[n];
     h = (int)(rem / per);
     rem -= per * h;
     int l;
@@ -153,6 +232,22 @@ struct Sched {
 
   // Next piece of this CTA's share; the same for every thread that calls it.
   __device__ bool next(Item* it) {
+    if (WAVES && wave < waves) {
+      find_unit(wave * G + (wave & 1 ? G - 1 - cta : cta));
+      ++wave;
+      int lo;
+      bool empty;
+      const int c = tiles(r, blk, &lo, &empty);
+      it->n = n;
+      it->h = h;
+      it->blk = blk;
+      it->r = r;
+      it->tb = empty ? 0 : lo;
+      it->te = empty ? 0 : lo + c;
+      it->whole = true;
+      it->slot = 0;
+      return true;
+    }
     if (pos >= end) return false;
     if (!started) {
       locate(pos);

@@ -11,8 +11,9 @@ probabilities):
   in the numerator and in the denominator;
 * so |delta lse_i| <= (d + 8) u X_i + (n + 32) u + u |lse_i|, and
   |delta o_ic| <= 2 A_ic ((d + 8) u X_i + (n + 32) u);
-* in bf16 the probabilities are rounded once more for the value product, 2^-9 A_ic, and
-  the output is rounded to bf16, 2^-9 |o_ic| (and 2^-9 of what it is off by already).
+* in bf16 the probabilities are rounded once more for the value product, 2^-8 A_ic, and
+  the output is rounded to bf16, 2^-8 |o_ic| (and 2^-8 of what it is off by already): bf16
+  has 8 significant bits, so a value of 1 and a bit moves by up to half of 2^-7.
 """
 import math
 
@@ -92,8 +93,8 @@ def bounds(o, lse, A, X, d, n, bf16):
     s = (d + 8) * U * X + (n + 32) * U
     t = 2 * A * s[..., None]
     if bf16:
-        t = t + 2.0 ** -9 * A
-        t = t + 2.0 ** -9 * (o.abs() + t)
+        t = t + 2.0 ** -8 * A
+        t = t + 2.0 ** -8 * (o.abs() + t)
     return t, s + U * lse.abs()
 
 
