@@ -18,11 +18,13 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBN = 64;
+constexpr int kBN = 64, kSimtRequests = 1024;
+template <int M>
+using SimtSched = Sched<M, kBN, kSimtRequests, false>;
 
 template <int D, int M>
 constexpr int simt_smem() {
-  return (M * D + kBN * (D + 4) + kBN * D + M * (kBN + 4)) * 4 + (int)sizeof(SchedMem<false>);
+  return (M * D + kBN * (D + 4) + kBN * D + M * (kBN + 4)) * 4 + (int)sizeof(typename SimtSched<M>::Mem);
 }
 
 // Four consecutive elements as fp32.
@@ -49,9 +51,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
   float* ks = qs + M * D;                      // [64][D + 4]
   float* vs = ks + kBN * (D + 4);              // [64][D]
   float* ps = vs + kBN * D;                    // [M][64 + 4]
-  auto* mem = reinterpret_cast<SchedMem<false>*>(ps + M * (kBN + 4));
+  auto* mem = reinterpret_cast<typename SimtSched<M>::Mem*>(ps + M * (kBN + 4));
 
-  Sched<M, kBN, false> sched;
+  SimtSched<M> sched;
   sched.template init<kThreads>(a.s, mem, blockIdx.x, gridDim.x);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   Item it;
@@ -228,7 +230,7 @@ cudaError_t launch_simt(const AttnArgs& a, bool bf16, int grid, cudaStream_t str
   }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<D, M, kBN, false>(a, bf16, grid, stream);
+  return launch_join<D, SimtSched<M>>(a, bf16, grid, stream);
 }
 
 template <int M>
@@ -242,29 +244,39 @@ cudaError_t launch_simt_d(const AttnArgs& a, int d, bool bf16, int grid, cudaStr
   }
 }
 
-int simt_grid() { return sm_count(); }
-
 size_t part_bytes(int grid, int M, int d) { return (size_t)2 * grid * M * (d + 2) * 4; }
 
 }  // namespace
 
-// Which kernels a call runs, from the most query rows of a request and key/value head:
-// the tensor-core kernel takes the requests with more than kShortRows rows, the CUDA-core
-// one the others and every other type and head size.
-constexpr int kShortRows = 16;
+// Which kernels a call runs, by the most query rows (tokens x heads of a group) of a request.
+//
+// bf16, d = 64 or 128: up to 16 or 32 rows the kernel for few rows, which is bound by HBM
+// and wastes no tensor-core rows; above, the tensor-core kernel, and for the requests of
+// the batch that have at most 16 rows the kernel for few rows after it.
+// fp32, and bf16 with d = 16 or 32: the CUDA-core kernel, with units of 16 rows where they
+// hold a request (few rows do not pay for 64) and of 64 above.
+struct Plan {
+  bool tc;
+  int mma;   // 16-row tiles of the kernel for few rows, 0: not run
+  int simt;  // rows of the CUDA-core kernel, 0: not run
+};
+Plan plan_of(int bf16, int d, long long rows) {
+  if (!bf16 || d < 64) return Plan{false, 0, rows <= 16 ? 16 : 64};
+  if (rows <= 32) return Plan{false, rows <= 16 ? 1 : 2, 0};
+  return Plan{true, 1, 0};
+}
 
 size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_len) {
-  const int grid = simt_grid();
-  const bool longer = (long long)max_q_len * (Hq / Hkv) > kShortRows;
-  if (bf16 && d >= 64)
-    return std::max(part_bytes(grid, 16, d), longer ? paged_tc_part_bytes(grid, d) : 0);
-  return part_bytes(grid, longer ? 64 : 16, d);
+  const int grid = sm_count();
+  const Plan p = plan_of(bf16, d, (long long)max_q_len * (Hq / Hkv));
+  if (p.simt) return part_bytes(grid, p.simt, d);
+  return std::max(paged_mma_part_bytes(p.mma, d), p.tc ? paged_tc_part_bytes(grid, d) : 0);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  const bool longer = (long long)a.max_q_len * (a.Hq / a.Hkv) > kShortRows;
-  const bool tc = longer && a.bf16 && a.d >= 64;
+  const Plan p = plan_of(a.bf16, a.d, (long long)a.max_q_len * (a.Hq / a.Hkv));
+  const int grid = sm_count();
   AttnArgs k{};
   k.q = a.q; k.kc = a.k_cache; k.vc = a.v_cache; k.out = a.out; k.lse = a.lse;
   k.q_stride = a.q_stride; k.Hq = a.Hq; k.bs = a.block_size; k.num_blocks = a.num_blocks;
@@ -272,29 +284,37 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.Hkv = a.Hkv; k.s.window = a.window;
   k.s.max_blocks = a.max_blocks; k.s.max_kv = (long long)a.max_blocks * a.block_size;
   k.s.min_tiles = 1;
-  const int grid = simt_grid(), M = longer && !tc ? 64 : 16;
   k.part_o = reinterpret_cast<float*>(a.workspace);
-  for (int n0 = 0; n0 < a.N; n0 += kSchedMax) {
-    k.s.nn = a.N - n0 < kSchedMax ? a.N - n0 : kSchedMax;
-    k.s.seq_lens = a.seq_lens + n0;
-    k.s.cu_seqlens = a.cu_seqlens + n0;
-    k.s.block_tables = a.block_tables + (size_t)n0 * a.max_blocks;
-    cudaError_t e = cudaSuccess;
-    if (tc) {
-      // one request: whatever its length is, so that nothing is left over
-      k.s.rows_lo = a.N > 1 ? kShortRows : 0;
-      k.s.rows_hi = 0x7fffffff;
-      if ((e = launch_paged_tc(k, a.d, grid, stream)) != cudaSuccess) return e;
-      if (a.N == 1) break;
+  auto ranges = [&](int most, int rows_lo, int rows_hi, auto launch) {
+    k.s.rows_lo = rows_lo;
+    k.s.rows_hi = rows_hi;
+    for (int n0 = 0; n0 < a.N; n0 += most) {
+      k.s.nn = std::min(a.N - n0, most);
+      k.s.seq_lens = a.seq_lens + n0;
+      k.s.cu_seqlens = a.cu_seqlens + n0;
+      k.s.block_tables = a.block_tables + (size_t)n0 * a.max_blocks;
+      const cudaError_t e = launch();
+      if (e != cudaSuccess) return e;
     }
-    k.s.rows_lo = 0;
-    k.s.rows_hi = tc ? kShortRows : 0x7fffffff;
-    k.part_ml = reinterpret_cast<float2*>(k.part_o + (size_t)2 * grid * M * a.d);
-    e = M == 16 ? launch_simt_d<16>(k, a.d, a.bf16, grid, stream)
-                : launch_simt_d<64>(k, a.d, a.bf16, grid, stream);
-    if (e != cudaSuccess) return e;
+    return cudaSuccess;
+  };
+  constexpr int kAll = 0x7fffffff;
+  cudaError_t e = cudaSuccess;
+  if (p.simt) {
+    k.part_ml = reinterpret_cast<float2*>(k.part_o + (size_t)2 * grid * p.simt * a.d);
+    return ranges(kSimtRequests, 0, kAll, [&] {
+      return p.simt == 16 ? launch_simt_d<16>(k, a.d, a.bf16, grid, stream)
+                          : launch_simt_d<64>(k, a.d, a.bf16, grid, stream);
+    });
   }
-  return cudaSuccess;
+  if (p.tc) {
+    // a single request is taken whatever its length, so that nothing is left over
+    e = ranges(paged_tc_requests(), a.N > 1 ? 16 : 0, kAll,
+               [&] { return launch_paged_tc(k, a.d, grid, stream); });
+    if (e != cudaSuccess || a.N == 1) return e;
+  }
+  return ranges(paged_mma_requests(), 0, p.tc ? 16 : kAll,
+                [&] { return launch_paged_mma(k, p.mma, a.d, stream); });
 }
 
 }  // namespace gdn

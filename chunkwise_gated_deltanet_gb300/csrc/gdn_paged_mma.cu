@@ -1,0 +1,400 @@
+// Attention of few query rows per request over the paged cache (bf16, d = 64 or 128): one
+// or a few new tokens, up to 16 or 32 (token, head of the group) rows a key/value head.
+//
+// Bound by HBM: every cached key and value is read once for at most 32 rows, 4 d x rows
+// operations against 4 d bytes a token.  The products run on mma.sync (m16n8k16), whose
+// 16-row tiles fit such units; tcgen05's 128 rows would be filled with zeros.  A CTA has
+// four warps and one for the loads; a tile is 64 cached tokens, of which each warp takes 16
+// through both products with a running maximum and sum of its own, so that nothing is
+// exchanged until the unit ends and the four results are joined in shared memory.  K and V
+// tiles come by TMA into a ring of 80 KB; two CTAs an SM keep 160 KB in flight, enough for
+// HBM's latency, and one's joins run under the other's loads.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <numeric>
+
+#include "paged_tiles.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kMmBN = 64, kMmWarps = 4, kMmThreads = 32 * (kMmWarps + 1), kMmRequests = 512;
+template <int MT>
+using MmSched = Sched<16 * MT, kMmBN, kMmRequests, false>;
+
+template <int D, int MT>
+struct MmSmem {
+  static constexpr int kPanel = kMmBN * 128;  // 64 rows of 64 bf16
+  static constexpr int kTile = kPanel * (D / 64);
+  static constexpr int kStages = 81920 / kTile;
+  static constexpr int kCols = MT == 1 ? 64 : 16;  // columns joined at a time
+  static constexpr int kRow = kCols + 8;           // padded: rows fall into different banks
+  uint8_t kv[kStages][kTile];
+  uint8_t q[(D / 64) * 16 * MT * 128];
+  float o[kMmWarps][16 * MT][kRow];
+  float2 ml[kMmWarps][16 * MT];
+  uint64_t full[kStages], empty[kStages];
+  typename MmSched<MT>::Mem sched;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One warp's 16 tokens of every tile.  When a wait gives up, the flow goes on with what is
+// in shared memory (later waits return at once), so that no barrier is left waiting; the
+// status word tells the host.
+template <int D, int MT>
+__device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sched) {
+  using S = MmSmem<D, MT>;
+  constexpr int M = 16 * MT, NT = D / 8;
+  volatile int* abort_flag = &sm.abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = a.s.g, window = a.s.window;
+  const float sl = a.scale_log2;
+  uint32_t kv = 0;
+  Item it;
+  while (sched.next(&it)) {
+    const int row0 = it.blk * M, past = it.r.kl - it.r.ql;
+    const int rows = min(it.r.rows - row0, M);
+    const int pos_first = past + row0 / g, pos_last = past + (row0 + rows - 1) / g;
+    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+    for (int e = tid; e < M * (D / 8); e += 32 * kMmWarps) {
+      const int rr = e / (D / 8), c = e % (D / 8), row = row0 + rr;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (rr < rows)
+        x = __ldg(reinterpret_cast<const uint4*>(
+            q + (size_t)(it.r.q0 + row / g) * a.q_stride + (size_t)(it.h * g + row % g) * D + c * 8));
+      st_shared_v4(smem_u32(sm.q + sw128_offset(rr, c * 8, M)), x.x, x.y, x.z, x.w);
+    }
+    named_sync(1, 32 * kMmWarps);
+    int pos[MT][2];
+    float m[MT][2], l[MT][2], o[MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int rr = 16 * i + 8 * u + (lane >> 2);
+        pos[i][u] = rr < rows ? past + (row0 + rr) / g : -1;
+        m[i][u] = -INFINITY;
+        l[i][u] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+    }
+    uint32_t qf[MT == 1 ? D / 16 : 1][4];
+    const int qr = (lane & 15), qc = (lane >> 4) * 8;
+    if (MT == 1) {
+#pragma unroll
+      for (int k = 0; k < (MT == 1 ? D / 16 : 1); ++k)
+        ldm4(smem_u32(sm.q + sw128_offset(qr, 16 * k + qc, M)), qf[k]);
+    }
+
+#pragma unroll 1
+    for (int t = it.tb; t < it.te; ++t, kv += 2) {
+      const uint32_t sk = kv % S::kStages, sv = (kv + 1) % S::kStages;
+      wait_bar(&sm.full[sk], (kv / S::kStages) & 1, abort_flag, false);
+      __syncwarp();
+      float s[MT][2][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
+      {
+        const uint8_t* kt = sm.kv[sk];
+        const int key = 16 * warp + (lane & 7) + ((lane >> 4) << 3), kc = ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          ldm4(smem_u32(kt + sw128_offset(key, 16 * k + kc, kMmBN)), b);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t qa[4];
+            if (MT == 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) qa[e] = qf[MT == 1 ? k : 0][e];
+            } else {
+              ldm4(smem_u32(sm.q + sw128_offset(16 * i + qr, 16 * k + qc, M)), qa);
+            }
+            mma16816(s[i][0], qa, b[0], b[1]);
+            mma16816(s[i][1], qa, b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[sk]);
+
+      const int j0 = t * kMmBN + 16 * warp;  // this warp's first token
+      const bool edge = edge_tile<kMmBN>(t, pos_first, pos_last, window);
+      uint32_t p[MT][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (edge) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int j = j0 + 8 * n + 2 * (lane & 3) + e;
+                if (j > pos[i][u] || (window > 0 && j <= pos[i][u] - window))
+                  s[i][n][2 * u + e] = -INFINITY;
+              }
+          }
+          float mx = fmaxf(fmaxf(s[i][0][2 * u], s[i][0][2 * u + 1]),
+                           fmaxf(s[i][1][2 * u], s[i][1][2 * u + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const bool up = mx > m[i][u];
+          if (__any_sync(0xffffffffu, up)) {
+            const float fade = up ? ex2((m[i][u] - mx) * sl) : 1.f;  // 0 from -inf
+            if (up) m[i][u] = mx;
+            l[i][u] *= fade;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              o[i][n][2 * u] *= fade;
+              o[i][n][2 * u + 1] *= fade;
+            }
+          }
+          const float off = m[i][u] == -INFINITY ? 0.f : -m[i][u] * sl;
+          float x[4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              x[2 * n + e] = ex2(fmaf(s[i][n][2 * u + e], sl, off));
+              l[i][u] += x[2 * n + e];
+            }
+          p[i][u] = pack_bf16(x[0], x[1]);
+          p[i][2 + u] = pack_bf16(x[2], x[3]);
+        }
+
+      wait_bar(&sm.full[sv], ((kv + 1) / S::kStages) & 1, abort_flag, false);
+      __syncwarp();
+      uint8_t* vt = sm.kv[sv];
+      if (edge) {
+        // 0 * inf must not reach a row through a token that it does not see: non-finite
+        // values are added to the rows that see them here, and are zeros in the product
+        bool found = false;
+#pragma unroll 1
+        for (int e = lane; e < 16 * (D / 8); e += 32) {
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              vt + sw128_offset(16 * warp + e % 16, (e / 16) * 8, kMmBN));
+          found |= not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+        }
+        if (__any_sync(0xffffffffu, found)) {
+#pragma unroll 1
+          for (int jj = 0; jj < 16; ++jj) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(
+                    vt + sw128_offset(16 * warp + jj, 8 * n + 2 * (lane & 3) + e, kMmBN));
+                const float x = __bfloat162float(*at);
+                __syncwarp();
+                if (!isfinite(x)) {
+#pragma unroll
+                  for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                      if (j0 + jj <= pos[i][u] && (window <= 0 || j0 + jj > pos[i][u] - window))
+                        o[i][n][2 * u + e] += x;
+                  *at = __float2bfloat16_rn(0.f);  // the eight lanes that hold this column
+                }
+              }
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
+      }
+      {
+        const int key = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8, vc = (lane >> 4) * 8;
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t b[4];
+          ldm4t(smem_u32(vt + sw128_offset(key, 8 * n + vc, kMmBN)), b);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            mma16816(o[i][n], p[i], b[0], b[1]);
+            mma16816(o[i][n + 1], p[i], b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[sv]);
+    }
+
+    // join the four warps, kCols columns at a time
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        l[i][u] += __shfl_xor_sync(0xffffffffu, l[i][u], 1);
+        l[i][u] += __shfl_xor_sync(0xffffffffu, l[i][u], 2);
+        if ((lane & 3) == 0) sm.ml[warp][16 * i + 8 * u + (lane >> 2)] = make_float2(m[i][u], l[i][u]);
+      }
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += S::kCols) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int rr = 16 * i + 8 * u + (lane >> 2);
+          if (rr < rows) {
+#pragma unroll
+            for (int n = 0; n < S::kCols / 8; ++n)
+              *reinterpret_cast<float2*>(&sm.o[warp][rr][8 * n + 2 * (lane & 3)]) =
+                  make_float2(o[i][c0 / 8 + n][2 * u], o[i][c0 / 8 + n][2 * u + 1]);
+          }
+        }
+      named_sync(1, 32 * kMmWarps);
+      for (int e = tid; e < rows * (S::kCols / 4); e += 32 * kMmWarps) {
+        const int rr = e / (S::kCols / 4), c = (e % (S::kCols / 4)) * 4;
+        float2 ml[kMmWarps];
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMmWarps; ++w) {
+          ml[w] = sm.ml[w][rr];
+          top = fmaxf(top, ml[w].x);
+        }
+        const float safe = top == -INFINITY ? 0.f : top;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kMmWarps; ++w) {
+          const float f = ex2((ml[w].x - safe) * sl);
+          const float4 y = *reinterpret_cast<const float4*>(&sm.o[w][rr][c]);
+          sum = fmaf(f, ml[w].y, sum);
+          x[0] = fmaf(f, y.x, x[0]);
+          x[1] = fmaf(f, y.y, x[1]);
+          x[2] = fmaf(f, y.z, x[2]);
+          x[3] = fmaf(f, y.w, x[3]);
+        }
+        const int row = row0 + rr;
+        if (it.whole) {
+          const size_t at = (size_t)(it.r.q0 + row / g) * a.Hq + it.h * g + row % g;
+          const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+          if (a.lse && c0 == 0 && c == 0) a.lse[at] = lse_of(top * sl, sum);
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + c0 + c) =
+              make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+        } else {
+          const size_t at = (size_t)it.slot * M + rr;
+          if (c0 == 0 && c == 0) a.part_ml[at] = make_float2(top * sl, sum);
+          st4(a.part_o + at * D + c0 + c, x[0], x[1], x[2], x[3]);
+        }
+      }
+      named_sync(1, 32 * kMmWarps);
+    }
+  }
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kMmThreads, 2)
+paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, int box, int* status) {
+  using S = MmSmem<D, MT>;
+  extern __shared__ uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) {
+    sm.abort_flag = 0;
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kMmWarps);
+    }
+    fence_mbarrier_init();
+    prefetch_tensormap(&mk);
+    prefetch_tensormap(&mv);
+  }
+  MmSched<MT> sched;
+  sched.template init<kMmThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);  // ends in a barrier
+  if (tid < 32 * kMmWarps) {
+    run_rows<D, MT>(sm, a, sched);
+  } else {
+    volatile int* abort_flag = &sm.abort_flag;
+    uint32_t kv = 0;
+    Item it;
+    while (sched.next(&it)) {
+      const PageLoads<D, kMmBN> pages(a, it, box);
+      int id0 = pages.page(it.tb, lane);
+      for (int t = it.tb; t < it.te; ++t) {
+        const int next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w, ++kv) {
+          const uint32_t slot = kv % S::kStages;
+          if (warp_wait_fails(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag, false)) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
+          __syncwarp();
+          pages.load(sm.kv[slot], w ? &mv : &mk, &sm.full[slot], t, lane, id0);
+        }
+        id0 = next0;
+      }
+    }
+  }
+  __syncthreads();
+  if (sm.abort_flag && tid == 0) {  // let copies still in flight land before the CTA ends
+    const uint64_t tw = globaltimer_ns();
+    while (globaltimer_ns() - tw < 50000ull) {
+    }
+    atomicOr(status, sm.abort_flag);
+  }
+}
+
+template <int D, int MT>
+cudaError_t launch_mma(AttnArgs a, cudaStream_t stream) {
+  constexpr int bytes = (int)sizeof(MmSmem<D, MT>) + 1024;
+  static_assert(2 * (bytes + 1024) <= 233472, "two CTAs an SM");
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = ensure_smem_cap(paged_mma_kernel<D, MT>, bytes, done, true);
+  if (e != cudaSuccess) return e;
+  int* status = nullptr;
+  if ((e = tc_status_address(&status)) != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  const int box = std::gcd(a.bs, kMmBN);
+  if (!make_page_map(&mk, a.kc, a.num_blocks, a.bs, a.s.Hkv, D, box) ||
+      !make_page_map(&mv, a.vc, a.num_blocks, a.bs, a.s.Hkv, D, box))
+    return cudaErrorInvalidValue;
+  const int grid = paged_mma_grid();
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * 16 * MT * D);
+  paged_mma_kernel<D, MT><<<grid, kMmThreads, bytes, stream>>>(a, mk, mv, box, status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_join<D, MmSched<MT>>(a, true, grid, stream);
+}
+
+}  // namespace
+
+int paged_mma_grid() { return 2 * sm_count(); }
+int paged_mma_requests() { return kMmRequests; }
+size_t paged_mma_part_bytes(int mt, int d) {
+  return (size_t)2 * paged_mma_grid() * 16 * mt * (d + 2) * 4;
+}
+
+cudaError_t launch_paged_mma(AttnArgs a, int mt, int d, cudaStream_t stream) {
+  if (d == 128) return mt == 1 ? launch_mma<128, 1>(a, stream) : launch_mma<128, 2>(a, stream);
+  return mt == 1 ? launch_mma<64, 1>(a, stream) : launch_mma<64, 2>(a, stream);
+}
+
+}  // namespace gdn

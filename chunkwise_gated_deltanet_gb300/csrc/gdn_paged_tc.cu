@@ -33,13 +33,13 @@
 #include <algorithm>
 #include <numeric>
 
-#include "paged_attn.cuh"
-#include "tc_common.cuh"
+#include "paged_tiles.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kTcM = 256, kTcBN = 128, kTcThreads = 384, kItems = 4;
+using TcSched = Sched<kTcM, kTcBN, 1024, true>;
 constexpr float kRaise = 8.f;  // log2 units by which a score may pass the running maximum
 
 struct TcItem {
@@ -57,7 +57,7 @@ struct TcSmem {
   uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
   uint64_t item_full[kItems], item_empty[kItems];
   TcItem items[kItems];
-  SchedMem<true> sched;
+  TcSched::Mem sched;
   uint32_t tmem;
   int abort_flag;
   int bad[kItems];  // a value that some row does not see is not finite
@@ -97,14 +97,6 @@ __device__ __forceinline__ bool wait_in(uint64_t* bar, uint32_t parity, volatile
 }
 __device__ __forceinline__ bool warp_waits(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait_in(bar, parity, abort_flag)) != 0;
-}
-
-// Whether tile `t` has tokens that some row of the unit does not see.
-__device__ __forceinline__ bool edge_tile(int t, int pos_first, int pos_last, int window) {
-  return t * kTcBN + kTcBN - 1 > pos_first || (window > 0 && t * kTcBN <= pos_last - window);
-}
-__device__ __forceinline__ bool not_finite(uint32_t two) {
-  return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
 }
 
 // Q rows of one half into its K-major tile: 16-byte pieces, rows past the unit as zeros.
@@ -178,7 +170,7 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
         tmem_wait_ld();
-        const bool edge = edge_tile(t, pos_first, pos_last, window);
+        const bool edge = edge_tile<kTcBN>(t, pos_first, pos_last, window);
         if (edge) {
           const int hi = pos - t * kTcBN;                            // columns seen: lo < c <= hi
           const int lo = window > 0 ? hi - window : -1;
@@ -303,7 +295,7 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
         const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(a.vc);
         const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
         for (int t = it.tb; t < it.te; ++t) {
-          if (!edge_tile(t, pos_first, pos_last, window)) continue;
+          if (!edge_tile<kTcBN>(t, pos_first, pos_last, window)) continue;
           for (int j = t * kTcBN; j < (t + 1) * kTcBN; ++j) {
             if (j > pos || (window > 0 && j <= pos - window)) continue;
             const int id = __ldg(table + j / a.bs);
@@ -405,16 +397,13 @@ __device__ void run_mma(TcSmem<D>& sm, uint32_t tmem) {
   }
 }
 
-// One warp: the schedule, and the loads of K and V tiles (rows of a page at a time; pages
-// past the sequence and table entries out of range read as zeros, by a coordinate past the
-// last page).
+// One warp: the schedule, and the loads of K and V tiles.
 template <int D>
-__device__ void run_loads(TcSmem<D>& sm, const AttnArgs& a, Sched<kTcM, kTcBN, true>& sched,
-                          const CUtensorMap* mk, const CUtensorMap* mv, int box) {
+__device__ void run_loads(TcSmem<D>& sm, const AttnArgs& a, TcSched& sched, const CUtensorMap* mk,
+                          const CUtensorMap* mv, int box) {
   using S = TcSmem<D>;
   volatile int* abort_flag = &sm.abort_flag;
   const int lane = threadIdx.x & 31;
-  const int per = kTcBN / box, boxes = per * (D / 64);  // a panel's, a tile's
   uint32_t kv = 0;
   for (uint32_t idx = 0;; ++idx) {
     Item it{};
@@ -427,28 +416,17 @@ __device__ void run_loads(TcSmem<D>& sm, const AttnArgs& a, Sched<kTcM, kTcBN, t
       mbar_arrive(&sm.item_full[idx % kItems]);
     }
     if (!valid) return;
-    const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
-    auto page = [&](int t, int e) {  // of box e of tile t
-      const int j = t * kTcBN + (e % per) * box;
-      int id = -1;
-      if (e < boxes && t < it.te && j < it.r.kl) id = __ldg(table + j / a.bs);
-      return id >= 0 && id < a.num_blocks ? id : a.num_blocks;
-    };
-    int id0 = page(it.tb, lane);
+    const PageLoads<D, kTcBN> pages(a, it, box);
+    int id0 = pages.page(it.tb, lane);
     for (int t = it.tb; t < it.te; ++t) {
-      const int next0 = page(t + 1, lane);  // in flight during this tile's waits
+      const int next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
 #pragma unroll 1
       for (int w = 0; w < 2; ++w, ++kv) {
         const uint32_t slot = kv % S::kStages;
         if (!warp_waits(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag)) return;
         if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
         __syncwarp();
-        for (int e = lane; e < boxes; e += 32) {
-          const int panel = e / per, rr = (e - panel * per) * box, j = t * kTcBN + rr;
-          const int id = e == lane ? id0 : page(t, e);
-          tma_load_4d(sm.kv[slot] + panel * S::kPanel + rr * 128, w ? mv : mk, &sm.full[slot], panel * 64,
-                      it.h, j % a.bs, id);
-        }
+        pages.load(sm.kv[slot], w ? mv : mk, &sm.full[slot], t, lane, id0);
       }
       id0 = next0;
     }
@@ -484,7 +462,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
     prefetch_tensormap(&mk);
     prefetch_tensormap(&mv);
   }
-  Sched<kTcM, kTcBN, true> sched;
+  TcSched sched;
   sched.template init<kTcThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);
   tc_fence_before();
   __syncthreads();
@@ -518,19 +496,6 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   }
 }
 
-// [num_blocks][bs][Hkv][D] bf16, boxes of 64 columns x 1 head x `box` tokens of one page.
-bool make_page_map(CUtensorMap* m, const void* base, int num_blocks, int bs, int Hkv, int D, int box_rows) {
-  auto enc = get_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)bs, (cuuint64_t)num_blocks};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)bs * Hkv * D * 2};
-  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch_tc_d(const AttnArgs& a, int grid, cudaStream_t stream) {
   constexpr int bytes = (int)sizeof(TcSmem<D>) + 1024;
@@ -546,12 +511,14 @@ cudaError_t launch_tc_d(const AttnArgs& a, int grid, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   paged_tc_kernel<D><<<grid, kTcThreads, bytes, stream>>>(a, mk, mv, box, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_join<D, kTcM, kTcBN, true>(a, true, grid, stream);
+  return launch_join<D, TcSched>(a, true, grid, stream);
 }
 
 }  // namespace
 
 size_t paged_tc_part_bytes(int grid, int d) { return (size_t)2 * grid * kTcM * (d + 2) * 4; }
+
+int paged_tc_requests() { return 1024; }
 
 cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream) {
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kTcM * d);

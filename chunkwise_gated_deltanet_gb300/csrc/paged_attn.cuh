@@ -23,9 +23,16 @@ struct AttnArgs {
   SchedArgs s;
 };
 
+// The kernel for few rows (bf16, d = 64 or 128): 16 mt rows a unit, mt = 1 or 2.
+int paged_mma_grid();
+size_t paged_mma_part_bytes(int mt, int d);
+int paged_mma_requests();  // requests a launch takes
+cudaError_t launch_paged_mma(AttnArgs a, int mt, int d, cudaStream_t stream);
+
 // The tensor-core kernel for chunks of new tokens (bf16, d = 64 or 128): partial-result
 // bytes for a grid, and its launch (a.part_o set; a.part_ml is placed behind it).
 size_t paged_tc_part_bytes(int grid, int d);
+int paged_tc_requests();
 cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream);
 
 namespace {
@@ -47,10 +54,11 @@ constexpr int kJoinRows = 8;  // rows a CTA joins, a warp each
 // Joins the partial results of the units that share boundaries cut: CTA (c - 1, y) looks
 // at the boundary between shares c - 1 and c, and if it is the first one inside its unit,
 // joins rows y * 8 .. y * 8 + 7 of it over every share that holds a part.
-template <int D, int M, int BN, bool BF16, bool WAVES>
+template <int D, typename SCHED, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnArgs a, int grid) {
-  __shared__ SchedMem<WAVES> mem;
-  Sched<M, BN, WAVES> sched;
+  constexpr int M = SCHED::kM;
+  __shared__ typename SCHED::Mem mem;
+  SCHED sched;
   sched.template init<kJoinThreads>(a.s, &mem, 0, grid);
   const int c = blockIdx.x + 1;
   if (c >= sched.G) return;
@@ -101,14 +109,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const AttnArgs
     if (lane + 32 * j < D) st_out<BF16>(a.out, at * D + lane + 32 * j, acc[j] * inv);
 }
 
-template <int D, int M, int BN, bool WAVES>
+template <int D, typename SCHED>
 cudaError_t launch_join(const AttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
   if (grid < 2) return cudaSuccess;
-  const dim3 g(grid - 1, M / kJoinRows);
+  const dim3 g(grid - 1, SCHED::kM / kJoinRows);
   if (bf16)
-    paged_join_kernel<D, M, BN, true, WAVES><<<g, kJoinThreads, 0, stream>>>(a, grid);
+    paged_join_kernel<D, SCHED, true><<<g, kJoinThreads, 0, stream>>>(a, grid);
   else
-    paged_join_kernel<D, M, BN, false, WAVES><<<g, kJoinThreads, 0, stream>>>(a, grid);
+    paged_join_kernel<D, SCHED, false><<<g, kJoinThreads, 0, stream>>>(a, grid);
   return cudaGetLastError();
 }
 

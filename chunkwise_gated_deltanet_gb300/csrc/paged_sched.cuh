@@ -25,8 +25,6 @@
 
 namespace gdn {
 
-constexpr int kSchedMax = 1024;  // requests of one launch
-
 struct SchedArgs {
   const int32_t* seq_lens;    // of this launch's first request
   const int32_t* cu_seqlens;
@@ -66,18 +64,21 @@ __device__ __forceinline__ Req load_req(const SchedArgs& s, int n) {
 }
 
 // Shared memory of a scheduler.
-template <bool WAVES>
+template <int NMAX, bool WAVES>
 struct SchedMem {
-  long long pre[kSchedMax + 1];            // tiles before each request
+  long long pre[NMAX + 1];            // tiles before each request
   long long warp[32];
-  int units[WAVES ? kSchedMax + 1 : 1];    // units before each request
+  int units[WAVES ? NMAX + 1 : 1];    // units before each request
   int warp_u[WAVES ? 32 : 1];
 };
 
-template <int M, int BN, bool WAVES>
+// M rows a unit, BN tokens a tile, NMAX requests a launch.
+template <int M, int BN, int NMAX, bool WAVES>
 struct Sched {
+  using Mem = SchedMem<NMAX, WAVES>;
+  static constexpr int kM = M;
   SchedArgs s;
-  const SchedMem<WAVES>* mem;
+  const Mem* mem;
   long long total, base, first, pos, end, unit0;
   int G, cta, n, h, blk;
   int waves, wave;
@@ -98,7 +99,7 @@ struct Sched {
 
   // Whole CTA of NT threads: prefix sums of the requests' tiles and units into `m`.
   template <int NT>
-  __device__ void init(const SchedArgs& args, SchedMem<WAVES>* m, int cta_id, int grid) {
+  __device__ void init(const SchedArgs& args, Mem* m, int cta_id, int grid) {
     s = args;
     mem = m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
