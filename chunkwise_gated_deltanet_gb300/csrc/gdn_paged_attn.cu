@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
 
   SimtSched<M> sched;
   sched.template init<kThreads>(a.s, mem, blockIdx.x, gridDim.x);
+  let_next_kernel_start();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   Item it;
   while (sched.next(&it)) {
@@ -281,7 +282,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   k.q = a.q; k.kc = a.k_cache; k.vc = a.v_cache; k.out = a.out; k.lse = a.lse;
   k.q_stride = a.q_stride; k.Hq = a.Hq; k.bs = a.block_size; k.num_blocks = a.num_blocks;
   k.scale_log2 = a.scale * 1.4426950408889634f;
-  k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.Hkv = a.Hkv; k.s.window = a.window;
+  k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.by_g = FastDiv((unsigned)k.s.g); k.s.Hkv = a.Hkv; k.s.window = a.window;
   k.s.max_blocks = a.max_blocks; k.s.max_kv = (long long)a.max_blocks * a.block_size;
   k.s.min_tiles = 1;
   k.part_o = reinterpret_cast<float*>(a.workspace);

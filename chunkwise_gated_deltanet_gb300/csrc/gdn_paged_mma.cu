@@ -331,6 +331,7 @@ paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
   }
   MmSched<MT> sched;
   sched.template init<kMmThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);  // ends in a barrier
+  let_next_kernel_start();
   if (tid < 32 * kMmWarps) {
     run_rows<D, MT>(sm, a, sched);
   } else {

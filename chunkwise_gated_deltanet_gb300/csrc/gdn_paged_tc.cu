@@ -464,6 +464,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   }
   TcSched sched;
   sched.template init<kTcThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);
+  let_next_kernel_start();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

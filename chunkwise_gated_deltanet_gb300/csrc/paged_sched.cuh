@@ -25,11 +25,26 @@
 
 namespace gdn {
 
+// Quotients by a divisor that the host knows, for dividends below 2^31: with l = ceil(log2 d)
+// and m = floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(m, n) + n) >> l.
+struct FastDiv {
+  unsigned d, m, l;
+  FastDiv() = default;
+  explicit FastDiv(unsigned div) : d(div), l(0) {
+    while ((1ull << l) < d) ++l;
+    m = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi(m, (unsigned)n) + (unsigned)n) >> l); }
+#endif
+};
+
 struct SchedArgs {
   const int32_t* seq_lens;    // of this launch's first request
   const int32_t* cu_seqlens;
   const int32_t* block_tables;
   int nn, T, g, Hkv, window, max_blocks;
+  FastDiv by_g;
   long long max_kv;           // max_blocks * block_size
   int rows_lo, rows_hi;       // requests with rows in (rows_lo, rows_hi] only
   int min_tiles;              // tiles a CTA takes at least (while there are that many)
@@ -79,8 +94,8 @@ struct Sched {
   static constexpr int kM = M;
   SchedArgs s;
   const Mem* mem;
-  long long total, base, first, pos, end, unit0;
-  int G, cta, n, h, blk;
+  long long total, base, quot, first, pos, end, unit0;
+  int G, rem, cta, n, h, blk;
   int waves, wave;
   Req r;
   bool started;
@@ -89,7 +104,7 @@ struct Sched {
   // is still written (`empty`).
   __device__ __forceinline__ int tiles(const Req& q, int b, int* lo, bool* empty) const {
     const int row0 = b * M, row1 = min(q.rows, row0 + M) - 1;
-    const int p0 = q.kl - q.ql + row0 / s.g, hi = q.kl - q.ql + row1 / s.g + 1;
+    const int p0 = q.kl - q.ql + s.by_g.div(row0), hi = q.kl - q.ql + s.by_g.div(row1) + 1;
     const int l = s.window > 0 ? max(0, p0 - s.window + 1) : 0;
     *empty = hi <= 0;
     *lo = *empty ? 0 : l / BN;
@@ -175,6 +190,8 @@ struct Sched {
         base = unit0;
       }
     }
+    quot = (total - base) / G;
+    rem = (int)(total - base - quot * G);
     wave = 0;
     first = cta < G ? share(cta) : total;
     pos = first;
@@ -182,56 +199,79 @@ struct Sched {
     if (cta >= G) waves = 0;
     started = false;
   }
-  __device__ __forceinline__ long long share(int c) const { return base + (total - base) * c / G; }
-
-  // Request, head, row block and first tile of unit `u`.
-  __device__ void find_unit(int u) {
-    int lo = 0, hi = s.nn;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (mem->units[mid] <= u)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    n = lo;
-    r = load_req(s, n);
-    const int rem = u - mem->units[n], nb = blocks(r);
-    h = rem / nb;
-    blk = rem - h * nb;
-    unit0 = mem->pre[n] + (mem->pre[n + 1] - mem->pre[n]) / s.Hkv * h;
-    int l;
-    bool e;
-    for (int b = 0; b < blk; ++b) unit0 += tiles(r, b, &l, &e);
+  // First tile of share c, and the share that holds tile x: shares differ by at most one tile.
+  __device__ __forceinline__ long long share(int c) const { return base + quot * c + min(c, rem); }
+  __device__ __forceinline__ int share_of(long long x) const {
+    const long long y = x - base, big = (quot + 1) * rem;
+    return (int)(y < big ? y / (quot + 1) : rem + (y - big) / quot);
   }
 
-  // Request, head, row block and start of the unit that holds tile `x`.
-  __device__ void locate(long long x) {
+  // Last request whose prefix is at most x.
+  template <typename V>
+  __device__ __forceinline__ int request_of(const V* p, V x) const {
     int lo = 0, hi = s.nn;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (mem->pre[mid] <= x)
+      if (p[mid] <= x)
         lo = mid;
       else
         hi = mid;
     }
-    n = lo;
+    return lo;
+  }
+  // Tiles of row blocks 0 .. upto - 1 of request r, by a whole warp.
+  __device__ int tiles_before(int upto) const {
+    int sum = 0;
+    for (int b = threadIdx.x & 31; b < upto; b += 32) {
+      int l;
+      bool e;
+      sum += tiles(r, b, &l, &e);
+    }
+    return __reduce_add_sync(0xffffffffu, sum);
+  }
+
+  // Request, head, row block and first tile of unit `u`; whole warps.
+  __device__ void find_unit(int u) {
+    n = request_of(mem->units, u);
+    r = load_req(s, n);
+    const int left = u - mem->units[n], nb = blocks(r);
+    h = left / nb;
+    blk = left - h * nb;
+    unit0 = mem->pre[n] + (mem->pre[n + 1] - mem->pre[n]) / s.Hkv * h + tiles_before(blk);
+  }
+
+  // Request, head, row block and start of the unit that holds tile `x`; whole warps.
+  __device__ void locate(long long x) {
+    n = request_of(mem->pre, x);
     r = load_req(s, n);
     const long long per = (mem->pre[n + 1] - mem->pre[n]) / s.Hkv;
-    long long rem = x - mem->pre[n];
-    h = (int)(rem / per);
-    rem -= per * h;
-    int l;
-    bool e;
-    for (blk = 0;; ++blk) {
-      const int c = tiles(r, blk, &l, &e);
-      if (rem < c) break;
-      rem -= c;
+    long long left = x - mem->pre[n];
+    h = (int)(left / per);
+    left -= per * h;
+    // 32 row blocks at a time: the first whose inclusive sum passes what is left
+    const int nb = blocks(r), lane = threadIdx.x & 31;
+    for (int b0 = 0;; b0 += 32) {
+      int l, c = 0;
+      bool e;
+      if (b0 + lane < nb) c = tiles(r, b0 + lane, &l, &e);
+      int inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, inc > left);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        blk = b0 + at;
+        unit0 = x - (left - (__shfl_sync(0xffffffffu, inc, at) - __shfl_sync(0xffffffffu, c, at)));
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    unit0 = x - rem;
   }
 
-  // Next piece of this CTA's share; the same for every thread that calls it.
+  // Next piece of this CTA's share, the same for every thread; whole warps.
   __device__ bool next(Item* it) {
     if (WAVES && wave < waves) {
       find_unit(wave * G + (wave & 1 ? G - 1 - cta : cta));
