@@ -230,10 +230,13 @@ paged_write_kernel(const uint8_t* __restrict__ k, const uint8_t* __restrict__ v,
 }  // namespace
 
 int sm_count() {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> count[kMaxDev];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 152;
+  if ((n = count[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  count[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
