@@ -25,8 +25,7 @@ using MmSched = Sched<16 * MT, kMmBN, kMmRequests, false>;
 
 template <int D, int MT>
 struct MmSmem {
-  static constexpr int kPanel = kMmBN * 128;  // 64 rows of 64 bf16
-  static constexpr int kTile = kPanel * (D / 64);
+  static constexpr int kTile = kMmBN * D * 2;
   static constexpr int kStages = 81920 / kTile;
   static constexpr int kCols = MT == 1 ? 64 : 16;  // columns joined at a time
   static constexpr int kRow = kCols + 8;           // padded: rows fall into different banks
@@ -129,7 +128,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t b[4];
-          ldm4(smem_u32(kt + sw128_offset(key, 16 * k + kc, kMmBN)), b);
+          ldm4(smem_u32(kt + tile_offset<D>(key, 16 * k + kc)), b);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             uint32_t qa[4];
@@ -202,7 +201,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
 #pragma unroll 1
         for (int e = lane; e < 16 * (D / 8); e += 32) {
           const uint4 x = *reinterpret_cast<const uint4*>(
-              vt + sw128_offset(16 * warp + e % 16, (e / 16) * 8, kMmBN));
+              vt + tile_offset<D>(16 * warp + e % 16, (e / 16) * 8));
           found |= not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
         }
         if (__any_sync(0xffffffffu, found)) {
@@ -213,7 +212,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(
-                    vt + sw128_offset(16 * warp + jj, 8 * n + 2 * (lane & 3) + e, kMmBN));
+                    vt + tile_offset<D>(16 * warp + jj, 8 * n + 2 * (lane & 3) + e));
                 const float x = __bfloat162float(*at);
                 __syncwarp();
                 if (!isfinite(x)) {
@@ -236,7 +235,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t b[4];
-          ldm4t(smem_u32(vt + sw128_offset(key, 8 * n + vc, kMmBN)), b);
+          ldm4t(smem_u32(vt + tile_offset<D>(key, 8 * n + vc)), b);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             mma16816(o[i][n], p[i], b[0], b[1]);
@@ -340,16 +339,16 @@ paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     Item it;
     while (sched.next(&it)) {
       const PageLoads<D, kMmBN> pages(a, it, box);
-      int id0 = pages.page(it.tb, lane);
+      int2 id0 = pages.page(it.tb, lane);
       for (int t = it.tb; t < it.te; ++t) {
-        const int next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
+        const int2 next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
 #pragma unroll 1
         for (int w = 0; w < 2; ++w, ++kv) {
           const uint32_t slot = kv % S::kStages;
           if (warp_wait_fails(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag, false)) break;
           if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
           __syncwarp();
-          pages.load(sm.kv[slot], w ? &mv : &mk, &sm.full[slot], t, lane, id0);
+          pages.load(sm.kv[slot], w ? &mv : &mk, &sm.full[slot], lane, id0);
         }
         id0 = next0;
       }

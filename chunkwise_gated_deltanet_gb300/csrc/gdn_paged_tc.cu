@@ -237,8 +237,8 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
           if (!waits(&sm.full[slot], (v / TcSmem<D>::kStages) & 1)) return;
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(sm.kv[slot] + (c >> 3) * TcSmem<D>::kPanel + wt * 128 +
-                                                 (((c + wt) & 7) << 4));
+            uint4* at = reinterpret_cast<uint4*>(
+                sm.kv[slot] + tile_offset<D>(wt, (c >> 3) * 64 + ((c + wt) & 7) * 8));
             const uint4 x = *at;
             if (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w)) {
               uint16_t* e = reinterpret_cast<uint16_t*>(at);
@@ -347,18 +347,18 @@ __device__ void run_mma(TcSmem<D>& sm, uint32_t tmem) {
   };
   auto scores = [&](uint32_t v, int half) {
     uint64_t q = smem_desc(smem_u32(sm.q[half]), 16, 1024);
-    uint64_t k = smem_desc(smem_u32(sm.kv[v % S::kStages]), 16, 1024);
+    uint64_t k = smem_desc(smem_u32(sm.kv[v % S::kStages]), 16, kGroupBytes<D>);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
       mma_bf16(tmem + half * 128, q + (i >> 2) * (S::kPanel >> 4) + kStepK * (i & 3),
-               k + (i >> 2) * (S::kPanel >> 4) + kStepK * (i & 3), id_s, i > 0);
+               k + (i >> 2) * (1024 >> 4) + kStepK * (i & 3), id_s, i > 0);
     mma_commit(&sm.s_full[half]);
   };
   auto values = [&](uint32_t v, int half, bool first) {
-    uint64_t b = smem_desc(smem_u32(sm.kv[v % S::kStages]), S::kPanel, 1024);
+    uint64_t b = smem_desc(smem_u32(sm.kv[v % S::kStages]), 1024, kGroupBytes<D>);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      mma_bf16_ta(tmem + 256 + half * 128, tmem + half * 128 + 8 * i, b + kStepMN * i, id_o,
+      mma_bf16_ta(tmem + 256 + half * 128, tmem + half * 128 + 8 * i, b + (2 * kGroupBytes<D> >> 4) * i, id_o,
                   !first || i > 0);
   };
   for (uint32_t idx = 0;; ++idx) {
@@ -417,16 +417,16 @@ __device__ void run_loads(TcSmem<D>& sm, const AttnArgs& a, TcSched& sched, cons
     }
     if (!valid) return;
     const PageLoads<D, kTcBN> pages(a, it, box);
-    int id0 = pages.page(it.tb, lane);
+    int2 id0 = pages.page(it.tb, lane);
     for (int t = it.tb; t < it.te; ++t) {
-      const int next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
+      const int2 next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
 #pragma unroll 1
       for (int w = 0; w < 2; ++w, ++kv) {
         const uint32_t slot = kv % S::kStages;
         if (!warp_waits(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag)) return;
         if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
         __syncwarp();
-        pages.load(sm.kv[slot], w ? mv : mk, &sm.full[slot], t, lane, id0);
+        pages.load(sm.kv[slot], w ? mv : mk, &sm.full[slot], lane, id0);
       }
       id0 = next0;
     }

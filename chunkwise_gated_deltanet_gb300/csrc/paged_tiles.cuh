@@ -17,43 +17,56 @@ __device__ __forceinline__ bool not_finite(uint32_t two) {
 }
 
 
-// [num_blocks][bs][Hkv][D] bf16, boxes of 64 columns x 1 head x `box` tokens of one page.
+// A K or V tile in shared memory: groups of 8 tokens, each D / 64 panels of 8 rows of 64 bf16
+// (128 bytes, 128-byte swizzle).  One TMA box fills all groups and panels that lie in one
+// page, so a tile of 128 tokens in pages of 16 takes 8 loads; with a panel of all rows after
+// the other, as 64-column boxes, it took 16, and issuing them bound the tensor-core kernel
+// (1440 us against 1110 us with pages of 32 for some 2000 new tokens of two requests).
+template <int D>
+constexpr int kGroupBytes = 1024 * (D / 64);
+template <int D>
+__device__ __forceinline__ uint32_t tile_offset(int row, int col) {
+  return (row >> 3) * kGroupBytes<D> + (col >> 6) * 1024 + (row & 7) * 128 +
+         ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+
+// [num_blocks][bs][Hkv][D] bf16 as (64 columns, 8 tokens, panels of all heads, groups, pages).
 bool make_page_map(CUtensorMap* m, const void* base, int num_blocks, int bs, int Hkv, int D, int box_rows) {
   auto enc = get_encoder();
   if (!enc) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)bs, (cuuint64_t)num_blocks};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)bs * Hkv * D * 2};
-  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+  const cuuint64_t token = (cuuint64_t)Hkv * D * 2;
+  const cuuint32_t panels = (cuuint32_t)D / 64;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)Hkv * panels, (cuuint64_t)bs / 8, (cuuint64_t)num_blocks};
+  cuuint64_t strides[4] = {token, 128, 8 * token, bs * token};
+  cuuint32_t box[5] = {64, 8, panels, (cuuint32_t)box_rows / 8, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Loads of one K or V tile of BN tokens by a whole warp: rows of a page at a time, as boxes
-// of `box` tokens x 64 columns.  Pages past the sequence and table entries out of range read
-// as zeros, through a coordinate past the last page.
+// Loads of one K or V tile of BN tokens by a whole warp, a box of `box` tokens each.  Pages
+// past the sequence and table entries out of range read as zeros, through a coordinate past
+// the last page.
 template <int D, int BN>
 struct PageLoads {
   const int32_t* table;
-  int kl, h, bs, num_blocks, box, per, boxes;
+  int kl, h, bs, num_blocks, box;
   __device__ PageLoads(const AttnArgs& a, const Item& it, int box_rows)
       : table(a.s.block_tables + (size_t)it.n * a.s.max_blocks), kl(it.r.kl), h(it.h), bs(a.bs),
-        num_blocks(a.num_blocks), box(box_rows), per(BN / box_rows), boxes(per * (D / 64)) {}
-  // Page of box `e` of tile `t`.
-  __device__ __forceinline__ int page(int t, int e) const {
-    const int j = t * BN + (e % per) * box;
-    const int id = e < boxes && j < kl ? __ldg(table + j / bs) : -1;
-    return id >= 0 && id < num_blocks ? id : num_blocks;
+        num_blocks(a.num_blocks), box(box_rows) {}
+  // Page and group of box `e` of tile `t` (BN / box <= 16 boxes: a lane each).
+  __device__ __forceinline__ int2 page(int t, int e) const {
+    const int j = t * BN + e * box;
+    const int blk = j / bs;
+    const int id = e * box < BN && j < kl ? __ldg(table + blk) : -1;
+    return make_int2(id >= 0 && id < num_blocks ? id : num_blocks, (j - blk * bs) >> 3);
   }
-  // `first`: page(t, lane), which the caller looked up ahead.
-  __device__ __forceinline__ void load(uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int t,
-                                       int lane, int first) const {
-    for (int e = lane; e < boxes; e += 32) {
-      const int panel = e / per, rr = (e - panel * per) * box;
-      const int id = e == lane ? first : page(t, e);
-      tma_load_4d(tile + panel * (BN * 128) + rr * 128, map, bar, panel * 64, h, (t * BN + rr) % bs, id);
-    }
+  // `at`: page(t, lane), which the caller looked up ahead.
+  __device__ __forceinline__ void load(uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int lane,
+                                       int2 at) const {
+    if (lane * box < BN)
+      tma_load_5d(tile + lane * (box / 8) * kGroupBytes<D>, map, bar, 0, 0, h * (D / 64), at.y, at.x);
   }
 };
 
