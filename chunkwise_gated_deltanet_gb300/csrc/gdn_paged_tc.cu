@@ -50,9 +50,11 @@ template <int D>
 struct TcSmem {
   static constexpr int kPanel = 128 * 128;             // 128 rows of 64 bf16
   static constexpr int kTile = kPanel * (D / 64);
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   uint8_t q[2][kTile];
-  uint8_t kv[kStages][kTile];
+  // a stage has V of a tile and K of the next one, which the MMA thread uses together: one
+  // wait and one release a tile (an item's first stage has K only, its last one V only)
+  uint8_t v[kStages][kTile], k[kStages][kTile];
   uint64_t full[kStages], empty[kStages];
   uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
   uint64_t item_full[kItems], item_empty[kItems];
@@ -140,7 +142,7 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
   };
   const float sl = a.scale_log2;
   const int g = a.s.g, window = a.s.window;
-  uint32_t ntile = 0, nitem = 0, kv = 0;  // tiles and items of this half; K/V loads of the CTA
+  uint32_t ntile = 0, nitem = 0, kv = 0;  // tiles and items of this half; K/V stages of the CTA
 
   if (!waits(&sm.item_full[0], 0)) return;
   auto active = [&](const TcItem& x) {
@@ -233,12 +235,12 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
         if (edge) {
           // 0 * inf must not reach a row through a token that it does not see: non-finite
           // values of this tile become zeros here and are added at the end, row by row
-          const uint32_t v = kv + 2 * (t - it.tb) + 1, slot = v % TcSmem<D>::kStages;
-          if (!waits(&sm.full[slot], (v / TcSmem<D>::kStages) & 1)) return;
+          const uint32_t st = kv + (t - it.tb) + 1, slot = st % TcSmem<D>::kStages;
+          if (!waits(&sm.full[slot], (st / TcSmem<D>::kStages) & 1)) return;
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) {
             uint4* at = reinterpret_cast<uint4*>(
-                sm.kv[slot] + tile_offset<D>(wt, (c >> 3) * 64 + ((c + wt) & 7) * 8));
+                sm.v[slot] + tile_offset<D>(wt, (c >> 3) * 64 + ((c + wt) & 7) * 8));
             const uint4 x = *at;
             if (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w)) {
               uint16_t* e = reinterpret_cast<uint16_t*>(at);
@@ -254,7 +256,7 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
         mbar_arrive(&sm.p_full[half]);
       }
     }
-    kv += 2 * (it.te - it.tb);
+    kv += it.te > it.tb ? it.te - it.tb + 1 : 0;
 
     // the next item's Q goes in before this one's output goes out
     const uint32_t nx = idx + 1;
@@ -340,22 +342,20 @@ __device__ void run_mma(TcSmem<D>& sm, uint32_t tmem) {
   constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
   volatile int* abort_flag = &sm.abort_flag;
   uint32_t kv = 0, nitem[2] = {0, 0}, np[2] = {0, 0};
-  auto wait_kv = [&](uint32_t v) {
-    const bool ok = wait_in(&sm.full[v % S::kStages], (v / S::kStages) & 1, abort_flag);
-    tc_fence_after();
-    return ok;
+  auto wait_stage = [&](uint32_t st) {
+    return wait_in(&sm.full[st % S::kStages], (st / S::kStages) & 1, abort_flag);
   };
-  auto scores = [&](uint32_t v, int half) {
-    uint64_t q = smem_desc(smem_u32(sm.q[half]), 16, 1024);
-    uint64_t k = smem_desc(smem_u32(sm.kv[v % S::kStages]), 16, kGroupBytes<D>);
+  auto scores = [&](uint32_t st, int half) {
+    const uint64_t q = smem_desc(smem_u32(sm.q[half]), 16, 1024);
+    const uint64_t k = smem_desc(smem_u32(sm.k[st % S::kStages]), 16, kGroupBytes<D>);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
       mma_bf16(tmem + half * 128, q + (i >> 2) * (S::kPanel >> 4) + kStepK * (i & 3),
                k + (i >> 2) * (1024 >> 4) + kStepK * (i & 3), id_s, i > 0);
     mma_commit(&sm.s_full[half]);
   };
-  auto values = [&](uint32_t v, int half, bool first) {
-    uint64_t b = smem_desc(smem_u32(sm.kv[v % S::kStages]), 1024, kGroupBytes<D>);
+  auto values = [&](uint32_t st, int half, bool first) {
+    const uint64_t b = smem_desc(smem_u32(sm.v[st % S::kStages]), 1024, kGroupBytes<D>);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       mma_bf16_ta(tmem + 256 + half * 128, tmem + half * 128 + 8 * i, b + (2 * kGroupBytes<D> >> 4) * i, id_o,
@@ -369,7 +369,7 @@ __device__ void run_mma(TcSmem<D>& sm, uint32_t tmem) {
     const int halves = it.rows - it.blk * kTcM > 128 ? 2 : 1;
     mbar_arrive(&sm.item_empty[idx % kItems]);
     if (tiles == 0) continue;
-    if (!wait_kv(kv)) return;
+    if (!wait_stage(kv)) return;
     for (int h = 0; h < halves; ++h) {
       if (!wait_in(&sm.q_full[h], nitem[h] & 1, abort_flag)) return;
       ++nitem[h];
@@ -377,22 +377,20 @@ __device__ void run_mma(TcSmem<D>& sm, uint32_t tmem) {
       scores(kv, h);
     }
     mma_commit(&sm.empty[kv % S::kStages]);
-    for (int j = 0; j < tiles; ++j, kv += 2) {
-      const bool more = j + 1 < tiles;
-      if (!wait_kv(kv + 1)) return;
-      if (more && !wait_kv(kv + 2)) return;
+    ++kv;
+    for (int j = 0; j < tiles; ++j, ++kv) {
+      if (!wait_stage(kv)) return;
       for (int h = 0; h < halves; ++h) {
         if (!wait_in(&sm.p_full[h], np[h] & 1, abort_flag)) return;
         ++np[h];
         tc_fence_after();
-        values(kv + 1, h, j == 0);
-        if (h == halves - 1) mma_commit(&sm.empty[(kv + 1) % S::kStages]);
-        if (more)
-          scores(kv + 2, h);
+        values(kv, h, j == 0);
+        if (j + 1 < tiles)
+          scores(kv, h);
         else
           mma_commit(&sm.o_full[h]);
       }
-      if (more) mma_commit(&sm.empty[(kv + 2) % S::kStages]);
+      mma_commit(&sm.empty[kv % S::kStages]);
     }
   }
 }
@@ -416,19 +414,20 @@ __device__ void run_loads(TcSmem<D>& sm, const AttnArgs& a, TcSched& sched, cons
       mbar_arrive(&sm.item_full[idx % kItems]);
     }
     if (!valid) return;
+    if (it.te == it.tb) continue;
     const PageLoads<D, kTcBN> pages(a, it, box);
-    int2 id0 = pages.page(it.tb, lane);
-    for (int t = it.tb; t < it.te; ++t) {
-      const int2 next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
-#pragma unroll 1
-      for (int w = 0; w < 2; ++w, ++kv) {
-        const uint32_t slot = kv % S::kStages;
-        if (!warp_waits(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag)) return;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
-        __syncwarp();
-        pages.load(sm.kv[slot], w ? mv : mk, &sm.full[slot], lane, id0);
-      }
-      id0 = next0;
+    int2 now = make_int2(0, 0), next = pages.page(it.tb, lane);
+    for (int t = it.tb - 1; t < it.te; ++t, ++kv) {  // V of tile t, K of tile t + 1
+      const int2 after = pages.page(t + 2, lane);    // in flight during this stage's wait
+      const bool v = t >= it.tb, k = t + 1 < it.te;
+      const uint32_t slot = kv % S::kStages;
+      if (!warp_waits(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag)) return;
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], v && k ? 2 * S::kTile : S::kTile);
+      __syncwarp();
+      if (k) pages.load(sm.k[slot], mk, &sm.full[slot], lane, next);
+      if (v) pages.load(sm.v[slot], mv, &sm.full[slot], lane, now);
+      now = next;
+      next = after;
     }
   }
 }
