@@ -104,28 +104,23 @@ __device__ __forceinline__ bool warp_waits(uint64_t* bar, uint32_t parity, volat
 // Q rows of one half into its K-major tile: 16-byte pieces, rows past the unit as zeros.
 template <int D>
 __device__ void load_q(const AttnArgs& a, const TcItem& it, int half, uint8_t* tile, int wt) {
-  constexpr int CH = D / 8;  // pieces a row
-  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
-  const int g = a.s.g, row0 = it.blk * kTcM + half * 128;
-#pragma unroll 1
-  for (int e0 = 0; e0 < 128 * CH; e0 += 128 * 8) {
-    uint4 x[8];
+  constexpr int CH = D / 8;  // pieces a row; a thread takes CH of them, all in flight at once
+  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + wt % CH * 8;
+  const int g = a.s.g, row0 = it.blk * kTcM + half * 128, rows = it.rows, head0 = it.h * g, q0 = it.q0;
+  uint4 x[CH];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int e = e0 + u * 128 + wt, rr = e / CH, c = e % CH, row = row0 + rr;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (row < it.rows) {
-        const int tok = row / g, head = it.h * g + (row - tok * g);
-        x[u] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)(it.q0 + tok) * a.q_stride +
-                                                    (size_t)head * D + c * 8));
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int e = e0 + u * 128 + wt, rr = e / CH, c = e % CH;
-      st_shared_v4(smem_u32(tile + sw128_offset(rr, c * 8, 128)), x[u].x, x[u].y, x[u].z, x[u].w);
+  for (int u = 0; u < CH; ++u) {
+    const int row = row0 + u * (128 / CH) + wt / CH;
+    x[u] = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      const int tok = a.s.by_g.div(row), head = head0 + (row - tok * g);
+      x[u] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)(q0 + tok) * a.q_stride + (size_t)head * D));
     }
   }
+#pragma unroll
+  for (int u = 0; u < CH; ++u)
+    st_shared_v4(smem_u32(tile + sw128_offset(u * (128 / CH) + wt / CH, wt % CH * 8, 128)), x[u].x, x[u].y,
+                 x[u].z, x[u].w);
   fence_async_smem();
 }
 

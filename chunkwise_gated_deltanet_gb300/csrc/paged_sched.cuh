@@ -15,7 +15,7 @@
 // w * CTAs + c to CTA c (odd waves the other way round), and shares only the last one to two
 // waves as above.  The CTAs then work on neighbouring row blocks of a few heads at a time
 // and read their keys and values from L2; contiguous shares would stream every head's cache
-// from HBM at once.
+// from HBM at once.  The shares of the rest make up for what the waves left uneven.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -78,6 +78,8 @@ __device__ __forceinline__ Req load_req(const SchedArgs& s, int n) {
   return r;
 }
 
+constexpr int kBalance = 256;  // CTAs up to which shares make up for uneven waves
+
 // Shared memory of a scheduler.
 template <int NMAX, bool WAVES>
 struct SchedMem {
@@ -85,6 +87,7 @@ struct SchedMem {
   long long warp[32];
   int units[WAVES ? NMAX + 1 : 1];    // units before each request
   int warp_u[WAVES ? 32 : 1];
+  long long bounds[WAVES ? kBalance + 1 : 1];  // first tiles of the shares after waves
 };
 
 // M rows a unit, BN tokens a tile, NMAX requests a launch.
@@ -98,7 +101,7 @@ struct Sched {
   int G, rem, cta, n, h, blk;
   int waves, wave;
   Req r;
-  bool started;
+  bool started, balanced;
 
   // Tiles [lo, lo + count) of row block `b`; count >= 1 so that a block that sees nothing
   // is still written (`empty`).
@@ -190,6 +193,28 @@ struct Sched {
         base = unit0;
       }
     }
+    balanced = WAVES && waves > 0 && G <= kBalance;
+    if (balanced) {
+      // share c: what CTA c's waves leave of an even part, one tile at least
+      long long x = 0;
+      if (tid < G) {
+        for (int w = 0; w < waves; ++w) x += unit_tiles(wave_unit(w, tid));
+        x = max((total + G - 1) / G - x, 1LL);
+      }
+      long long inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      __syncthreads();  // the sums of tokens have been read
+      if (lane == 31) m->warp[warp] = inc;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) inc += m->warp[w];
+      if (tid < G) m->bounds[tid] = min(total, base + inc - x);
+      if (tid == 0) m->bounds[G] = total;
+      __syncthreads();
+    }
     quot = (total - base) / G;
     rem = (int)(total - base - quot * G);
     wave = 0;
@@ -199,17 +224,30 @@ struct Sched {
     if (cta >= G) waves = 0;
     started = false;
   }
-  // First tile of share c, and the share that holds tile x: shares differ by at most one tile.
-  __device__ __forceinline__ long long share(int c) const { return base + quot * c + min(c, rem); }
+  // First tile of share c, and the share that holds tile x (without waves, shares differ by at
+  // most one tile).
+  __device__ __forceinline__ long long share(int c) const {
+    return balanced ? mem->bounds[c] : base + quot * c + min(c, rem);
+  }
   __device__ __forceinline__ int share_of(long long x) const {
+    if (balanced) return last_upto(mem->bounds, G, x);
     const long long y = x - base, big = (quot + 1) * rem;
     return (int)(y < big ? y / (quot + 1) : rem + (y - big) / quot);
   }
 
-  // Last request whose prefix is at most x.
+  __device__ __forceinline__ int wave_unit(int w, int c) const { return w * G + (w & 1 ? G - 1 - c : c); }
+  // Tiles of unit `u`.
+  __device__ int unit_tiles(int u) const {
+    const int q = last_upto(mem->units, s.nn, u);
+    const Req a = load_req(s, q);
+    int l;
+    bool e;
+    return tiles(a, (u - mem->units[q]) % blocks(a), &l, &e);
+  }
+  // Last of the first n entries of an ascending array that is at most x.
   template <typename V>
-  __device__ __forceinline__ int request_of(const V* p, V x) const {
-    int lo = 0, hi = s.nn;
+  __device__ __forceinline__ static int last_upto(const V* p, int n, V x) {
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (p[mid] <= x)
@@ -232,7 +270,7 @@ struct Sched {
 
   // Request, head, row block and first tile of unit `u`; whole warps.
   __device__ void find_unit(int u) {
-    n = request_of(mem->units, u);
+    n = last_upto(mem->units, s.nn, u);
     r = load_req(s, n);
     const int left = u - mem->units[n], nb = blocks(r);
     h = left / nb;
@@ -242,7 +280,7 @@ struct Sched {
 
   // Request, head, row block and start of the unit that holds tile `x`; whole warps.
   __device__ void locate(long long x) {
-    n = request_of(mem->pre, x);
+    n = last_upto(mem->pre, s.nn, x);
     r = load_req(s, n);
     const long long per = (mem->pre[n + 1] - mem->pre[n]) / s.Hkv;
     long long left = x - mem->pre[n];
@@ -274,7 +312,7 @@ struct Sched {
   // Next piece of this CTA's share, the same for every thread; whole warps.
   __device__ bool next(Item* it) {
     if (WAVES && wave < waves) {
-      find_unit(wave * G + (wave & 1 ? G - 1 - cta : cta));
+      find_unit(wave_unit(wave, cta));
       ++wave;
       int lo;
       bool empty;
