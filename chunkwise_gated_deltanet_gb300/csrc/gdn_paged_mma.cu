@@ -7,7 +7,7 @@
 // four warps and one for the loads; a tile is 64 cached tokens, of which each warp takes 16
 // through both products with a running maximum and sum of its own, so that nothing is
 // exchanged until the unit ends and the four results are joined in shared memory.  K and V
-// tiles come by TMA into a ring of 80 KB; two CTAs an SM keep 160 KB in flight, enough for
+// tiles come by TMA into a ring of 64 or 80 KB; two CTAs an SM keep twice that in flight, enough for
 // HBM's latency, and one's joins run under the other's loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -23,14 +23,20 @@ constexpr int kMmBN = 64, kMmWarps = 4, kMmThreads = 32 * (kMmWarps + 1), kMmReq
 template <int MT>
 using MmSched = Sched<16 * MT, kMmBN, kMmRequests, false>;
 
+struct MmItem {
+  int valid, h, row0, rows, q0, past, tb, te, whole, slot;
+};
+
 template <int D, int MT>
 struct MmSmem {
   static constexpr int kTile = kMmBN * D * 2;
-  static constexpr int kStages = 81920 / kTile;
+  static constexpr int kStages = (MT == 1 ? 81920 : 65536) / kTile;
   static constexpr int kCols = MT == 1 ? 64 : 16;  // columns joined at a time
   static constexpr int kRow = kCols + 8;           // padded: rows fall into different banks
   uint8_t kv[kStages][kTile];
-  uint8_t q[(D / 64) * 16 * MT * 128];
+  uint8_t q[2][(D / 64) * 16 * MT * 128];
+  MmItem items[2];
+  uint64_t item_full[2], item_empty[2];
   float o[kMmWarps][16 * MT][kRow];
   float2 ml[kMmWarps][16 * MT];
   uint64_t full[kStages], empty[kStages];
@@ -60,10 +66,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // One warp's 16 tokens of every tile.  When a wait gives up, the flow goes on with what is
-// in shared memory (later waits return at once), so that no barrier is left waiting; the
-// status word tells the host.
+// in shared memory to the end of the item (later waits return at once), so that no barrier
+// is left waiting; the status word tells the host.
 template <int D, int MT>
-__device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sched) {
+__device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a) {
   using S = MmSmem<D, MT>;
   constexpr int M = 16 * MT, NT = D / 8;
   volatile int* abort_flag = &sm.abort_flag;
@@ -71,21 +77,15 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
   const int g = a.s.g, window = a.s.window;
   const float sl = a.scale_log2;
   uint32_t kv = 0;
-  Item it;
-  while (sched.next(&it)) {
-    const int row0 = it.blk * M, past = it.r.kl - it.r.ql;
-    const int rows = min(it.r.rows - row0, M);
-    const int pos_first = past + row0 / g, pos_last = past + (row0 + rows - 1) / g;
-    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
-    for (int e = tid; e < M * (D / 8); e += 32 * kMmWarps) {
-      const int rr = e / (D / 8), c = e % (D / 8), row = row0 + rr;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (rr < rows)
-        x = __ldg(reinterpret_cast<const uint4*>(
-            q + (size_t)(it.r.q0 + row / g) * a.q_stride + (size_t)(it.h * g + row % g) * D + c * 8));
-      st_shared_v4(smem_u32(sm.q + sw128_offset(rr, c * 8, M)), x.x, x.y, x.z, x.w);
-    }
-    named_sync(1, 32 * kMmWarps);
+  for (uint32_t idx = 0;; ++idx) {
+    wait_bar(&sm.item_full[idx & 1], (idx >> 1) & 1, abort_flag, false);
+    // one vote, so that no warp leaves while another goes on to the barriers below
+    if (named_sync_or(1, 32 * kMmWarps, *abort_flag != 0)) break;
+    const MmItem it = sm.items[idx & 1];
+    if (!it.valid) break;
+    const uint8_t* qs = sm.q[idx & 1];
+    const int row0 = it.row0, rows = it.rows, past = it.past;
+    const int pos_first = past + a.s.by_g.div(row0), pos_last = past + a.s.by_g.div(row0 + rows - 1);
     int pos[MT][2];
     float m[MT][2], l[MT][2], o[MT][NT][4];
 #pragma unroll
@@ -93,7 +93,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int rr = 16 * i + 8 * u + (lane >> 2);
-        pos[i][u] = rr < rows ? past + (row0 + rr) / g : -1;
+        pos[i][u] = rr < rows ? past + a.s.by_g.div(row0 + rr) : -1;
         m[i][u] = -INFINITY;
         l[i][u] = 0.f;
       }
@@ -107,7 +107,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
     if (MT == 1) {
 #pragma unroll
       for (int k = 0; k < (MT == 1 ? D / 16 : 1); ++k)
-        ldm4(smem_u32(sm.q + sw128_offset(qr, 16 * k + qc, M)), qf[k]);
+        ldm4(smem_u32(qs + sw128_offset(qr, 16 * k + qc, M)), qf[k]);
     }
 
 #pragma unroll 1
@@ -136,7 +136,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
 #pragma unroll
               for (int e = 0; e < 4; ++e) qa[e] = qf[MT == 1 ? k : 0][e];
             } else {
-              ldm4(smem_u32(sm.q + sw128_offset(16 * i + qr, 16 * k + qc, M)), qa);
+              ldm4(smem_u32(qs + sw128_offset(16 * i + qr, 16 * k + qc, M)), qa);
             }
             mma16816(s[i][0], qa, b[0], b[1]);
             mma16816(s[i][1], qa, b[2], b[3]);
@@ -149,6 +149,8 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
       const int j0 = t * kMmBN + 16 * warp;  // this warp's first token
       const bool edge = edge_tile<kMmBN>(t, pos_first, pos_last, window);
       uint32_t p[MT][4];
+      float mx[MT][2];
+      bool raise = false;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -163,14 +165,31 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
                   s[i][n][2 * u + e] = -INFINITY;
               }
           }
-          float mx = fmaxf(fmaxf(s[i][0][2 * u], s[i][0][2 * u + 1]),
+          mx[i][u] = fmaxf(fmaxf(s[i][0][2 * u], s[i][0][2 * u + 1]),
                            fmaxf(s[i][1][2 * u], s[i][1][2 * u + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const bool up = mx > m[i][u];
-          if (__any_sync(0xffffffffu, up)) {
-            const float fade = up ? ex2((m[i][u] - mx) * sl) : 1.f;  // 0 from -inf
-            if (up) m[i][u] = mx;
+        }
+#pragma unroll
+      for (int by = 1; by <= 2; by <<= 1)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            mx[i][u] = fmaxf(mx[i][u], __shfl_xor_sync(0xffffffffu, mx[i][u], by));
+      // the maximum is raised only when a score passes it by more than kRaise (log2 units): P
+      // and l may then be up to 2^8 larger, of the same relative precision
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          raise |= (mx[i][u] - m[i][u]) * sl > kRaise || (m[i][u] == -INFINITY && mx[i][u] != -INFINITY);
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const bool up = (mx[i][u] - m[i][u]) * sl > kRaise || (m[i][u] == -INFINITY && mx[i][u] != -INFINITY);
+            const float fade = up ? ex2((m[i][u] - mx[i][u]) * sl) : 1.f;  // 0 from -inf
+            if (up) m[i][u] = mx[i][u];
             l[i][u] *= fade;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -178,15 +197,18 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
               o[i][n][2 * u + 1] *= fade;
             }
           }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
           const float off = m[i][u] == -INFINITY ? 0.f : -m[i][u] * sl;
           float x[4];
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x[2 * n + e] = ex2(fmaf(s[i][n][2 * u + e], sl, off));
-              l[i][u] += x[2 * n + e];
-            }
+            for (int e = 0; e < 2; ++e) x[2 * n + e] = ex2(fmaf(s[i][n][2 * u + e], sl, off));
+          l[i][u] += (x[0] + x[1]) + (x[2] + x[3]);
           p[i][u] = pack_bf16(x[0], x[1]);
           p[i][2 + u] = pack_bf16(x[2], x[3]);
         }
@@ -247,6 +269,9 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
       if (lane == 0) mbar_arrive(&sm.empty[sv]);
     }
 
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[idx & 1]);
+
     // join the four warps, kCols columns at a time
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -294,7 +319,8 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
         }
         const int row = row0 + rr;
         if (it.whole) {
-          const size_t at = (size_t)(it.r.q0 + row / g) * a.Hq + it.h * g + row % g;
+          const int tok = a.s.by_g.div(row);
+          const size_t at = (size_t)(it.q0 + tok) * a.Hq + it.h * g + (row - tok * g);
           const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
           if (a.lse && c0 == 0 && c == 0) a.lse[at] = lse_of(top * sl, sum);
           *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + c0 + c) =
@@ -310,6 +336,57 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sche
   }
 }
 
+// One warp: the schedule, each item's Q rows into shared memory (ahead of the warps that use
+// them), and the loads of K and V tiles.
+template <int D, int MT>
+__device__ void run_loads(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sched, const CUtensorMap* mk,
+                          const CUtensorMap* mv, int box) {
+  using S = MmSmem<D, MT>;
+  constexpr int M = 16 * MT, CH = D / 8, PER = M * CH / 32;  // 16-byte pieces a row, a lane
+  volatile int* abort_flag = &sm.abort_flag;
+  const int lane = threadIdx.x & 31, g = a.s.g;
+  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+  uint32_t kv = 0;
+  for (uint32_t idx = 0;; ++idx) {
+    Item it{};
+    const bool valid = sched.next(&it);
+    const int row0 = it.blk * M, rows = min(it.r.rows - row0, M);
+    uint4 x[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int e = u * 32 + lane, rr = e / CH, tok = a.s.by_g.div(row0 + rr);
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (valid && rr < rows)
+        x[u] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)(it.r.q0 + tok) * a.q_stride +
+                                                    (size_t)(it.h * g + (row0 + rr - tok * g)) * D + e % CH * 8));
+    }
+    if (warp_wait_fails(&sm.item_empty[idx & 1], ((idx >> 1) & 1) ^ 1, abort_flag, false)) return;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int e = u * 32 + lane;
+      st_shared_v4(smem_u32(sm.q[idx & 1] + sw128_offset(e / CH, e % CH * 8, M)), x[u].x, x[u].y, x[u].z, x[u].w);
+    }
+    if (lane == 0)
+      sm.items[idx & 1] = MmItem{valid, it.h, row0, rows, it.r.q0, it.r.kl - it.r.ql, it.tb, it.te, it.whole, it.slot};
+    mbar_arrive(&sm.item_full[idx & 1]);  // every lane, for its rows
+    if (!valid) return;
+    const PageLoads<D, kMmBN> pages(a, it, box);
+    int2 id0 = pages.page(it.tb, lane);
+    for (int t = it.tb; t < it.te; ++t) {
+      const int2 next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w, ++kv) {
+        const uint32_t slot = kv % S::kStages;
+        if (warp_wait_fails(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag, false)) return;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
+        __syncwarp();
+        pages.load(sm.kv[slot], w ? mv : mk, &sm.full[slot], lane, id0);
+      }
+      id0 = next0;
+    }
+  }
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(kMmThreads, 2)
 paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
@@ -317,12 +394,16 @@ paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
   using S = MmSmem<D, MT>;
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   if (tid == 0) {
     sm.abort_flag = 0;
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], kMmWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.item_full[i], 32);
+      mbar_init(&sm.item_empty[i], kMmWarps);
     }
     fence_mbarrier_init();
     prefetch_tensormap(&mk);
@@ -332,27 +413,9 @@ paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
   sched.template init<kMmThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);  // ends in a barrier
   let_next_kernel_start();
   if (tid < 32 * kMmWarps) {
-    run_rows<D, MT>(sm, a, sched);
+    run_rows<D, MT>(sm, a);
   } else {
-    volatile int* abort_flag = &sm.abort_flag;
-    uint32_t kv = 0;
-    Item it;
-    while (sched.next(&it)) {
-      const PageLoads<D, kMmBN> pages(a, it, box);
-      int2 id0 = pages.page(it.tb, lane);
-      for (int t = it.tb; t < it.te; ++t) {
-        const int2 next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
-#pragma unroll 1
-        for (int w = 0; w < 2; ++w, ++kv) {
-          const uint32_t slot = kv % S::kStages;
-          if (warp_wait_fails(&sm.empty[slot], ((kv / S::kStages) & 1) ^ 1, abort_flag, false)) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], S::kTile);
-          __syncwarp();
-          pages.load(sm.kv[slot], w ? &mv : &mk, &sm.full[slot], lane, id0);
-        }
-        id0 = next0;
-      }
-    }
+    run_loads<D, MT>(sm, a, sched, &mk, &mv, box);
   }
   __syncthreads();
   if (sm.abort_flag && tid == 0) {  // let copies still in flight land before the CTA ends

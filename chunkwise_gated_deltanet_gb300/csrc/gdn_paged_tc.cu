@@ -40,7 +40,6 @@ namespace {
 
 constexpr int kTcM = 256, kTcBN = 128, kTcThreads = 384, kItems = 4;
 using TcSched = Sched<kTcM, kTcBN, 1024, true>;
-constexpr float kRaise = 8.f;  // log2 units by which a score may pass the running maximum
 
 struct TcItem {
   int valid, n, h, blk, q0, ql, kl, rows, tb, te, whole, slot;

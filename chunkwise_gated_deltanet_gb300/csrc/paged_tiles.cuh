@@ -7,6 +7,8 @@
 namespace gdn {
 namespace {
 
+constexpr float kRaise = 8.f;  // log2 units by which a score may pass the running maximum
+
 // Whether tile `t` has tokens that some row of the unit does not see.
 template <int BN>
 __device__ __forceinline__ bool edge_tile(int t, int pos_first, int pos_last, int window) {
