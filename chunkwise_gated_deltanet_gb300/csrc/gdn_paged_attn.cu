@@ -251,27 +251,25 @@ size_t part_bytes(int grid, int M, int d) { return (size_t)2 * grid * M * (d + 2
 
 // Which kernels a call runs, by the most query rows (tokens x heads of a group) of a request.
 //
-// bf16, d = 64 or 128: up to 16 or 32 rows the kernel for few rows, which is bound by HBM
-// and wastes no tensor-core rows; above, the tensor-core kernel, and for the requests of
-// the batch that have at most 16 rows the kernel for few rows after it.
+// bf16, d = 64 or 128: up to 16 rows the kernel for few rows, which wastes no tensor-core
+// rows; above, the tensor-core kernel, and for the requests of the batch that have at most 16
+// rows the kernel for few rows after it.
 // fp32, and bf16 with d = 16 or 32: the CUDA-core kernel, with units of 16 rows where they
 // hold a request (few rows do not pay for 64) and of 64 above.
 struct Plan {
   bool tc;
-  int mma;   // 16-row tiles of the kernel for few rows, 0: not run
   int simt;  // rows of the CUDA-core kernel, 0: not run
 };
 Plan plan_of(int bf16, int d, long long rows) {
-  if (!bf16 || d < 64) return Plan{false, 0, rows <= 16 ? 16 : 64};
-  if (rows <= 32) return Plan{false, rows <= 16 ? 1 : 2, 0};
-  return Plan{true, 1, 0};
+  if (!bf16 || d < 64) return Plan{false, rows <= 16 ? 16 : 64};
+  return Plan{rows > 16, 0};
 }
 
 size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_len) {
   const int grid = sm_count();
   const Plan p = plan_of(bf16, d, (long long)max_q_len * (Hq / Hkv));
   if (p.simt) return part_bytes(grid, p.simt, d);
-  return std::max(paged_mma_part_bytes(p.mma, d), p.tc ? paged_tc_part_bytes(grid, d) : 0);
+  return std::max(paged_mma_part_bytes(d), p.tc ? paged_tc_part_bytes(grid, d) : 0);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
@@ -315,7 +313,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess || a.N == 1) return e;
   }
   return ranges(paged_mma_requests(), 0, p.tc ? 16 : kAll,
-                [&] { return launch_paged_mma(k, p.mma, a.d, stream); });
+                [&] { return launch_paged_mma(k, a.d, stream); });
 }
 
 }  // namespace gdn

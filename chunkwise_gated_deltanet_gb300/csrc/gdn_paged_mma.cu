@@ -1,14 +1,15 @@
 // Attention of few query rows per request over the paged cache (bf16, d = 64 or 128): one
-// or a few new tokens, up to 16 or 32 (token, head of the group) rows a key/value head.
+// or a few new tokens, up to 16 (token, head of the group) rows a key/value head.
 //
-// Bound by HBM: every cached key and value is read once for at most 32 rows, 4 d x rows
+// Bound by HBM: every cached key and value is read once for at most 16 rows, 4 d x rows
 // operations against 4 d bytes a token.  The products run on mma.sync (m16n8k16), whose
-// 16-row tiles fit such units; tcgen05's 128 rows would be filled with zeros.  A CTA has
-// four warps and one for the loads; a tile is 64 cached tokens, of which each warp takes 16
+// 16-row tiles fit such units; of tcgen05's 128 rows most would be zeros.  A CTA has four
+// warps and one for the loads; a tile is 64 cached tokens, of which each warp takes 16
 // through both products with a running maximum and sum of its own, so that nothing is
 // exchanged until the unit ends and the four results are joined in shared memory.  K and V
-// tiles come by TMA into a ring of 64 or 80 KB; two CTAs an SM keep twice that in flight, enough for
-// HBM's latency, and one's joins run under the other's loads.
+// tiles come by TMA into a ring of 80 KB; two CTAs an SM keep 160 KB in flight, enough for
+// HBM's latency, and one's joins run under the other's loads.  The load warp works one item
+// ahead: it has looked up the next one's lengths, pages and Q rows before it needs them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,27 +21,27 @@ namespace gdn {
 namespace {
 
 constexpr int kMmBN = 64, kMmWarps = 4, kMmThreads = 32 * (kMmWarps + 1), kMmRequests = 512;
-template <int MT>
-using MmSched = Sched<16 * MT, kMmBN, kMmRequests, false>;
+constexpr int kMmM = 16;  // rows a unit
+using MmSched = Sched<kMmM, kMmBN, kMmRequests, false>;
 
 struct MmItem {
   int valid, h, row0, rows, q0, past, tb, te, whole, slot;
 };
 
-template <int D, int MT>
+template <int D>
 struct MmSmem {
   static constexpr int kTile = kMmBN * D * 2;
-  static constexpr int kStages = (MT == 1 ? 81920 : 65536) / kTile;
-  static constexpr int kCols = MT == 1 ? 64 : 16;  // columns joined at a time
-  static constexpr int kRow = kCols + 8;           // padded: rows fall into different banks
+  static constexpr int kStages = 81920 / kTile;
+  static constexpr int kCols = 64;        // columns joined at a time
+  static constexpr int kRow = kCols + 8;  // padded: rows fall into different banks
   uint8_t kv[kStages][kTile];
-  uint8_t q[2][(D / 64) * 16 * MT * 128];
+  uint8_t q[2][(D / 64) * kMmM * 128];
   MmItem items[2];
   uint64_t item_full[2], item_empty[2];
-  float o[kMmWarps][16 * MT][kRow];
-  float2 ml[kMmWarps][16 * MT];
+  float o[kMmWarps][kMmM][kRow];
+  float2 ml[kMmWarps][kMmM];
   uint64_t full[kStages], empty[kStages];
-  typename MmSched<MT>::Mem sched;
+  MmSched::Mem sched;
   int abort_flag;
 };
 
@@ -68,14 +69,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // One warp's 16 tokens of every tile.  When a wait gives up, the flow goes on with what is
 // in shared memory to the end of the item (later waits return at once), so that no barrier
 // is left waiting; the status word tells the host.
-template <int D, int MT>
-__device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a) {
-  using S = MmSmem<D, MT>;
-  constexpr int M = 16 * MT, NT = D / 8;
+template <int D>
+__device__ void run_rows(MmSmem<D>& sm, const AttnArgs& a) {
+  using S = MmSmem<D>;
+  constexpr int M = kMmM, NT = D / 8, NK = D / 16;
   volatile int* abort_flag = &sm.abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = a.s.g, window = a.s.window;
   const float sl = a.scale_log2;
+  // the lane's places in a tile: rows of K for ldmatrix, rows of V for its transposed form
+  const int kkey = 16 * warp + (lane & 7) + ((lane >> 4) << 3), kcol = ((lane >> 3) & 1) * 8;
+  const int vkey = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8, vcol = (lane >> 4) * 8;
   uint32_t kv = 0;
   for (uint32_t idx = 0;; ++idx) {
     wait_bar(&sm.item_full[idx & 1], (idx >> 1) & 1, abort_flag, false);
@@ -83,135 +87,108 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a) {
     if (named_sync_or(1, 32 * kMmWarps, *abort_flag != 0)) break;
     const MmItem it = sm.items[idx & 1];
     if (!it.valid) break;
-    const uint8_t* qs = sm.q[idx & 1];
     const int row0 = it.row0, rows = it.rows, past = it.past;
     const int pos_first = past + a.s.by_g.div(row0), pos_last = past + a.s.by_g.div(row0 + rows - 1);
-    int pos[MT][2];
-    float m[MT][2], l[MT][2], o[MT][NT][4];
+    // rows lane / 4 and lane / 4 + 8 are this lane's (u = 0, 1)
+    int pos[2];
+    float m[2], l[2], o[NT][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int rr = 16 * i + 8 * u + (lane >> 2);
-        pos[i][u] = rr < rows ? past + a.s.by_g.div(row0 + rr) : -1;
-        m[i][u] = -INFINITY;
-        l[i][u] = 0.f;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+    for (int u = 0; u < 2; ++u) {
+      const int rr = 8 * u + (lane >> 2);
+      pos[u] = rr < rows ? past + a.s.by_g.div(row0 + rr) : -1;
+      m[u] = -INFINITY;
+      l[u] = 0.f;
     }
-    uint32_t qf[MT == 1 ? D / 16 : 1][4];
-    const int qr = (lane & 15), qc = (lane >> 4) * 8;
-    if (MT == 1) {
 #pragma unroll
-      for (int k = 0; k < (MT == 1 ? D / 16 : 1); ++k)
-        ldm4(smem_u32(qs + sw128_offset(qr, 16 * k + qc, M)), qf[k]);
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    uint32_t qf[NK][4];
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+      ldm4(smem_u32(sm.q[idx & 1] + sw128_offset(lane & 15, 16 * k + (lane >> 4) * 8, M)), qf[k]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[idx & 1]);
 
 #pragma unroll 1
     for (int t = it.tb; t < it.te; ++t, kv += 2) {
       const uint32_t sk = kv % S::kStages, sv = (kv + 1) % S::kStages;
       wait_bar(&sm.full[sk], (kv / S::kStages) & 1, abort_flag, false);
       __syncwarp();
-      float s[MT][2][4];
+      float s[2][4];
+      {
+        float part[2][2][4];  // two chains of products for each 8 tokens
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[c][n][e] = 0.f;
+        uint32_t b[NK][4];
+#pragma unroll
+        for (int k = 0; k < NK; ++k) ldm4(smem_u32(sm.kv[sk] + tile_offset<D>(kkey, 16 * k + kcol)), b[k]);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          mma16816(part[k & 1][0], qf[k], b[k][0], b[k][1]);
+          mma16816(part[k & 1][1], qf[k], b[k][2], b[k][3]);
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-      {
-        const uint8_t* kt = sm.kv[sk];
-        const int key = 16 * warp + (lane & 7) + ((lane >> 4) << 3), kc = ((lane >> 3) & 1) * 8;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          ldm4(smem_u32(kt + tile_offset<D>(key, 16 * k + kc)), b);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t qa[4];
-            if (MT == 1) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) qa[e] = qf[MT == 1 ? k : 0][e];
-            } else {
-              ldm4(smem_u32(qs + sw128_offset(16 * i + qr, 16 * k + qc, M)), qa);
-            }
-            mma16816(s[i][0], qa, b[0], b[1]);
-            mma16816(s[i][1], qa, b[2], b[3]);
-          }
-        }
+          for (int e = 0; e < 4; ++e) s[n][e] = part[0][n][e] + part[1][n][e];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[sk]);
 
       const int j0 = t * kMmBN + 16 * warp;  // this warp's first token
       const bool edge = edge_tile<kMmBN>(t, pos_first, pos_last, window);
-      uint32_t p[MT][4];
-      float mx[MT][2];
-      bool raise = false;
+      if (edge) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (edge) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int j = j0 + 8 * n + 2 * (lane & 3) + e;
-                if (j > pos[i][u] || (window > 0 && j <= pos[i][u] - window))
-                  s[i][n][2 * u + e] = -INFINITY;
-              }
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + 8 * n + 2 * (lane & 3) + (e & 1), at = pos[e >> 1];
+            if (j > at || (window > 0 && j <= at - window)) s[n][e] = -INFINITY;
           }
-          mx[i][u] = fmaxf(fmaxf(s[i][0][2 * u], s[i][0][2 * u + 1]),
-                           fmaxf(s[i][1][2 * u], s[i][1][2 * u + 1]));
-        }
+      }
+      float mx[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        mx[u] = fmaxf(fmaxf(s[0][2 * u], s[0][2 * u + 1]), fmaxf(s[1][2 * u], s[1][2 * u + 1]));
 #pragma unroll
       for (int by = 1; by <= 2; by <<= 1)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            mx[i][u] = fmaxf(mx[i][u], __shfl_xor_sync(0xffffffffu, mx[i][u], by));
+        for (int u = 0; u < 2; ++u) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], by));
       // the maximum is raised only when a score passes it by more than kRaise (log2 units): P
       // and l may then be up to 2^8 larger, of the same relative precision
+      bool up[2];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          raise |= (mx[i][u] - m[i][u]) * sl > kRaise || (m[i][u] == -INFINITY && mx[i][u] != -INFINITY);
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const bool up = (mx[i][u] - m[i][u]) * sl > kRaise || (m[i][u] == -INFINITY && mx[i][u] != -INFINITY);
-            const float fade = up ? ex2((m[i][u] - mx[i][u]) * sl) : 1.f;  // 0 from -inf
-            if (up) m[i][u] = mx[i][u];
-            l[i][u] *= fade;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              o[i][n][2 * u] *= fade;
-              o[i][n][2 * u + 1] *= fade;
-            }
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int u = 0; u < 2; ++u)
+        up[u] = (mx[u] - m[u]) * sl > kRaise || (m[u] == -INFINITY && mx[u] != -INFINITY);
+      if (__any_sync(0xffffffffu, up[0] || up[1])) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float off = m[i][u] == -INFINITY ? 0.f : -m[i][u] * sl;
-          float x[4];
+          const float fade = up[u] ? ex2((m[u] - mx[u]) * sl) : 1.f;  // 0 from -inf
+          if (up[u]) m[u] = mx[u];
+          l[u] *= fade;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[2 * n + e] = ex2(fmaf(s[i][n][2 * u + e], sl, off));
-          l[i][u] += (x[0] + x[1]) + (x[2] + x[3]);
-          p[i][u] = pack_bf16(x[0], x[1]);
-          p[i][2 + u] = pack_bf16(x[2], x[3]);
+          for (int n = 0; n < NT; ++n) {
+            o[n][2 * u] *= fade;
+            o[n][2 * u + 1] *= fade;
+          }
         }
+      }
+      uint32_t p[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float off = m[u] == -INFINITY ? 0.f : -m[u] * sl;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = ex2(fmaf(s[e >> 1][2 * u + (e & 1)], sl, off));
+        l[u] += (x[0] + x[1]) + (x[2] + x[3]);
+        p[u] = pack_bf16(x[0], x[1]);
+        p[2 + u] = pack_bf16(x[2], x[3]);
+      }
 
       wait_bar(&sm.full[sv], ((kv + 1) / S::kStages) & 1, abort_flag, false);
       __syncwarp();
@@ -222,8 +199,7 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a) {
         bool found = false;
 #pragma unroll 1
         for (int e = lane; e < 16 * (D / 8); e += 32) {
-          const uint4 x = *reinterpret_cast<const uint4*>(
-              vt + tile_offset<D>(16 * warp + e % 16, (e / 16) * 8));
+          const uint4 x = *reinterpret_cast<const uint4*>(vt + tile_offset<D>(16 * warp + e % 16, (e / 16) * 8));
           found |= not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
         }
         if (__any_sync(0xffffffffu, found)) {
@@ -239,12 +215,9 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a) {
                 __syncwarp();
                 if (!isfinite(x)) {
 #pragma unroll
-                  for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                      if (j0 + jj <= pos[i][u] && (window <= 0 || j0 + jj > pos[i][u] - window))
-                        o[i][n][2 * u + e] += x;
-                  *at = __float2bfloat16_rn(0.f);  // the eight lanes that hold this column
+                  for (int u = 0; u < 2; ++u)
+                    if (j0 + jj <= pos[u] && (window <= 0 || j0 + jj > pos[u] - window)) o[n][2 * u + e] += x;
+                  *at = __float2bfloat16_rn(0.f);  // by the eight lanes that hold this column
                 }
               }
           }
@@ -252,49 +225,40 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a) {
           __syncwarp();
         }
       }
-      {
-        const int key = 16 * warp + (lane & 7) + ((lane >> 3) & 1) * 8, vc = (lane >> 4) * 8;
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t b[4];
-          ldm4t(smem_u32(vt + tile_offset<D>(key, 8 * n + vc)), b);
+      for (int n0 = 0; n0 < NT; n0 += 8) {
+        uint32_t b[4][4];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            mma16816(o[i][n], p[i], b[0], b[1]);
-            mma16816(o[i][n + 1], p[i], b[2], b[3]);
-          }
+        for (int n = 0; n < 4; ++n) ldm4t(smem_u32(vt + tile_offset<D>(vkey, 8 * n0 + 16 * n + vcol)), b[n]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          mma16816(o[n0 + 2 * n], p, b[n][0], b[n][1]);
+          mma16816(o[n0 + 2 * n + 1], p, b[n][2], b[n][3]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[sv]);
     }
 
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.item_empty[idx & 1]);
-
     // join the four warps, kCols columns at a time
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        l[i][u] += __shfl_xor_sync(0xffffffffu, l[i][u], 1);
-        l[i][u] += __shfl_xor_sync(0xffffffffu, l[i][u], 2);
-        if ((lane & 3) == 0) sm.ml[warp][16 * i + 8 * u + (lane >> 2)] = make_float2(m[i][u], l[i][u]);
-      }
+    for (int u = 0; u < 2; ++u) {
+      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
+      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+      if ((lane & 3) == 0) sm.ml[warp][8 * u + (lane >> 2)] = make_float2(m[u], l[u]);
+    }
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += S::kCols) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int u = 0; u < 2; ++u) {
+        const int rr = 8 * u + (lane >> 2);
+        if (rr < rows) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int rr = 16 * i + 8 * u + (lane >> 2);
-          if (rr < rows) {
-#pragma unroll
-            for (int n = 0; n < S::kCols / 8; ++n)
-              *reinterpret_cast<float2*>(&sm.o[warp][rr][8 * n + 2 * (lane & 3)]) =
-                  make_float2(o[i][c0 / 8 + n][2 * u], o[i][c0 / 8 + n][2 * u + 1]);
-          }
+          for (int n = 0; n < S::kCols / 8; ++n)
+            *reinterpret_cast<float2*>(&sm.o[warp][rr][8 * n + 2 * (lane & 3)]) =
+                make_float2(o[c0 / 8 + n][2 * u], o[c0 / 8 + n][2 * u + 1]);
         }
+      }
       named_sync(1, 32 * kMmWarps);
       for (int e = tid; e < rows * (S::kCols / 4); e += 32 * kMmWarps) {
         const int rr = e / (S::kCols / 4), c = (e % (S::kCols / 4)) * 4;
@@ -338,28 +302,33 @@ __device__ void run_rows(MmSmem<D, MT>& sm, const AttnArgs& a) {
 
 // One warp: the schedule, each item's Q rows into shared memory (ahead of the warps that use
 // them), and the loads of K and V tiles.
-template <int D, int MT>
-__device__ void run_loads(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sched, const CUtensorMap* mk,
+template <int D>
+__device__ void run_loads(MmSmem<D>& sm, const AttnArgs& a, MmSched& sched, const CUtensorMap* mk,
                           const CUtensorMap* mv, int box) {
-  using S = MmSmem<D, MT>;
-  constexpr int M = 16 * MT, CH = D / 8, PER = M * CH / 32;  // 16-byte pieces a row, a lane
+  using S = MmSmem<D>;
+  constexpr int M = kMmM, CH = D / 8, PER = M * CH / 32;  // 16-byte pieces a row, a lane
   volatile int* abort_flag = &sm.abort_flag;
   const int lane = threadIdx.x & 31, g = a.s.g;
   const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
-  uint32_t kv = 0;
-  for (uint32_t idx = 0;; ++idx) {
-    Item it{};
-    const bool valid = sched.next(&it);
-    const int row0 = it.blk * M, rows = min(it.r.rows - row0, M);
-    uint4 x[PER];
+  Item it{};
+  bool valid;
+  uint4 x[PER];  // the coming item's Q rows
+  auto look_ahead = [&](Item& to) {
+    const bool ok = sched.next(&to);
+    const int row0 = to.blk * M, rows = min(to.r.rows - row0, M);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int e = u * 32 + lane, rr = e / CH, tok = a.s.by_g.div(row0 + rr);
       x[u] = make_uint4(0, 0, 0, 0);
-      if (valid && rr < rows)
-        x[u] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)(it.r.q0 + tok) * a.q_stride +
-                                                    (size_t)(it.h * g + (row0 + rr - tok * g)) * D + e % CH * 8));
+      if (ok && rr < rows)
+        x[u] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)(to.r.q0 + tok) * a.q_stride +
+                                                    (size_t)(to.h * g + (row0 + rr - tok * g)) * D + e % CH * 8));
     }
+    return ok;
+  };
+  valid = look_ahead(it);
+  uint32_t kv = 0;
+  for (uint32_t idx = 0;; ++idx) {
     if (warp_wait_fails(&sm.item_empty[idx & 1], ((idx >> 1) & 1) ^ 1, abort_flag, false)) return;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
@@ -367,10 +336,13 @@ __device__ void run_loads(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sch
       st_shared_v4(smem_u32(sm.q[idx & 1] + sw128_offset(e / CH, e % CH * 8, M)), x[u].x, x[u].y, x[u].z, x[u].w);
     }
     if (lane == 0)
-      sm.items[idx & 1] = MmItem{valid, it.h, row0, rows, it.r.q0, it.r.kl - it.r.ql, it.tb, it.te, it.whole, it.slot};
+      sm.items[idx & 1] = MmItem{valid,        it.h,  it.blk * M, min(it.r.rows - it.blk * M, M), it.r.q0,
+                                 it.r.kl - it.r.ql, it.tb, it.te,      it.whole,                         it.slot};
     mbar_arrive(&sm.item_full[idx & 1]);  // every lane, for its rows
     if (!valid) return;
     const PageLoads<D, kMmBN> pages(a, it, box);
+    Item next{};
+    bool more = false;
     int2 id0 = pages.page(it.tb, lane);
     for (int t = it.tb; t < it.te; ++t) {
       const int2 next0 = pages.page(t + 1, lane);  // in flight during this tile's waits
@@ -383,15 +355,19 @@ __device__ void run_loads(MmSmem<D, MT>& sm, const AttnArgs& a, MmSched<MT>& sch
         pages.load(sm.kv[slot], w ? mv : mk, &sm.full[slot], lane, id0);
       }
       id0 = next0;
+      if (t == it.tb) more = look_ahead(next);
     }
+    if (it.tb == it.te) more = look_ahead(next);
+    it = next;
+    valid = more;
   }
 }
 
-template <int D, int MT>
+template <int D>
 __global__ void __launch_bounds__(kMmThreads, 2)
 paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, int box, int* status) {
-  using S = MmSmem<D, MT>;
+  using S = MmSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x;
@@ -409,13 +385,13 @@ paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     prefetch_tensormap(&mk);
     prefetch_tensormap(&mv);
   }
-  MmSched<MT> sched;
+  MmSched sched;
   sched.template init<kMmThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);  // ends in a barrier
   let_next_kernel_start();
   if (tid < 32 * kMmWarps) {
-    run_rows<D, MT>(sm, a);
+    run_rows<D>(sm, a);
   } else {
-    run_loads<D, MT>(sm, a, sched, &mk, &mv, box);
+    run_loads<D>(sm, a, sched, &mk, &mv, box);
   }
   __syncthreads();
   if (sm.abort_flag && tid == 0) {  // let copies still in flight land before the CTA ends
@@ -426,12 +402,14 @@ paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
   }
 }
 
-template <int D, int MT>
+int mma_grid() { return 2 * sm_count(); }
+
+template <int D>
 cudaError_t launch_mma(AttnArgs a, cudaStream_t stream) {
-  constexpr int bytes = (int)sizeof(MmSmem<D, MT>) + 1024;
+  constexpr int bytes = (int)sizeof(MmSmem<D>) + 1024;
   static_assert(2 * (bytes + 1024) <= 233472, "two CTAs an SM");
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = ensure_smem_cap(paged_mma_kernel<D, MT>, bytes, done, true);
+  cudaError_t e = ensure_smem_cap(paged_mma_kernel<D>, bytes, done, true);
   if (e != cudaSuccess) return e;
   int* status = nullptr;
   if ((e = tc_status_address(&status)) != cudaSuccess) return e;
@@ -440,24 +418,20 @@ cudaError_t launch_mma(AttnArgs a, cudaStream_t stream) {
   if (!make_page_map(&mk, a.kc, a.num_blocks, a.bs, a.s.Hkv, D, box) ||
       !make_page_map(&mv, a.vc, a.num_blocks, a.bs, a.s.Hkv, D, box))
     return cudaErrorInvalidValue;
-  const int grid = paged_mma_grid();
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * 16 * MT * D);
-  paged_mma_kernel<D, MT><<<grid, kMmThreads, bytes, stream>>>(a, mk, mv, box, status);
+  const int grid = mma_grid();
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kMmM * D);
+  paged_mma_kernel<D><<<grid, kMmThreads, bytes, stream>>>(a, mk, mv, box, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_join<D, MmSched<MT>>(a, true, grid, stream);
+  return launch_join<D, MmSched>(a, true, grid, stream);
 }
 
 }  // namespace
 
-int paged_mma_grid() { return 2 * sm_count(); }
 int paged_mma_requests() { return kMmRequests; }
-size_t paged_mma_part_bytes(int mt, int d) {
-  return (size_t)2 * paged_mma_grid() * 16 * mt * (d + 2) * 4;
-}
+size_t paged_mma_part_bytes(int d) { return (size_t)2 * mma_grid() * kMmM * (d + 2) * 4; }
 
-cudaError_t launch_paged_mma(AttnArgs a, int mt, int d, cudaStream_t stream) {
-  if (d == 128) return mt == 1 ? launch_mma<128, 1>(a, stream) : launch_mma<128, 2>(a, stream);
-  return mt == 1 ? launch_mma<64, 1>(a, stream) : launch_mma<64, 2>(a, stream);
+cudaError_t launch_paged_mma(AttnArgs a, int d, cudaStream_t stream) {
+  return d == 128 ? launch_mma<128>(a, stream) : launch_mma<64>(a, stream);
 }
 
 }  // namespace gdn

@@ -9,11 +9,13 @@
 // does.  So a unit has 256 rows as two halves of 128, each with a warpgroup of its own (a
 // thread a row: no exchange for the row's maximum and sum): while one half's softmax runs,
 // the tensor cores work on the other half's products.  The halves share the K and V tiles,
-// which also halves the reads from L2.
+// which also halves the reads from L2.  A unit of at most 128 rows is taken by both halves as
+// well, every second tile each, and their results are joined in shared memory: with one half
+// alone nothing would run under its softmax.
 //
 //   warps 0-3, 4-7  softmax of the two halves: Q into shared memory, S out of TMEM, P into
 //                   it, and the output
-//   warp 8          one thread issues every MMA
+//   warp 8          issues every MMA
 //   warp 9          schedules, looks up pages and issues the TMA loads
 //   (warps 10, 11 fill the third warpgroup, which hands registers to the other two:
 //   384 threads x 168 = 256 x 200 + 128 x 104)
@@ -43,6 +45,9 @@ using TcSched = Sched<kTcM, kTcBN, 1024, true>;
 
 struct TcItem {
   int valid, n, h, blk, q0, ql, kl, rows, tb, te, whole, slot;
+  // At most 128 rows: both halves take them, half h every second tile from tile h on.
+  __device__ __forceinline__ bool solo() const { return rows - blk * kTcM <= 128; }
+  __device__ __forceinline__ bool active(int half) const { return te - tb > (solo() ? half : 0); }
 };
 
 template <int D>
@@ -56,12 +61,14 @@ struct TcSmem {
   uint8_t v[kStages][kTile], k[kStages][kTile];
   uint64_t full[kStages], empty[kStages];
   uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
+  uint64_t sum_full, sum_empty;  // half 1's part of a solo unit, in its Q's place
   uint64_t item_full[kItems], item_empty[kItems];
   TcItem items[kItems];
   TcSched::Mem sched;
   uint32_t tmem;
   int abort_flag;
   int bad[kItems];  // a value that some row does not see is not finite
+  float2 ml[128];   // half 1's maxima and sums of a solo unit
 };
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -136,28 +143,29 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
   };
   const float sl = a.scale_log2;
   const int g = a.s.g, window = a.s.window;
-  uint32_t ntile = 0, nitem = 0, kv = 0;  // tiles and items of this half; K/V stages of the CTA
+  uint32_t ntile = 0, nitem = 0, nsum = 0, kv = 0;  // tiles, items and joins of this half; K/V stages
 
-  if (!waits(&sm.item_full[0], 0)) return;
-  auto active = [&](const TcItem& x) {
-    return x.te > x.tb && x.rows - x.blk * kTcM > half * 128;
+  // Q of an item: each half its rows, of a solo unit half 0 alone
+  auto next_q = [&](const TcItem& x) {
+    if (x.valid && x.active(half) && !(x.solo() && half == 1)) {
+      load_q<D>(a, x, half, sm.q[half], wt);
+      mbar_arrive(&sm.q_full[half]);
+    }
   };
-  if (sm.items[0].valid && active(sm.items[0])) {
-    load_q<D>(a, sm.items[0], half, sm.q[half], wt);
-    mbar_arrive(&sm.q_full[half]);
-  }
+  if (!waits(&sm.item_full[0], 0)) return;
+  next_q(sm.items[0]);
   for (uint32_t idx = 0;; ++idx) {
     const TcItem& it = sm.items[idx % kItems];  // stays in shared memory: registers are S's
     if (!it.valid) break;
-    const int past = it.kl - it.ql, row = it.blk * kTcM + half * 128 + wt;
-    const int pos_first = past + it.blk * kTcM / g;
-    const int pos_last = past + (min(it.rows, it.blk * kTcM + kTcM) - 1) / g;
-    const int pos = past + row / g;
-    const bool on = active(it);
+    const bool solo = it.solo(), on = it.active(half);
+    const int past = it.kl - it.ql, row = it.blk * kTcM + (solo ? 0 : half * 128) + wt;
+    const int pos_first = past + a.s.by_g.div(it.blk * kTcM);
+    const int pos_last = past + a.s.by_g.div(min(it.rows, it.blk * kTcM + kTcM) - 1);
+    const int pos = past + a.s.by_g.div(row);
     float m = -INFINITY, l = 0.f;
     if (on) {
 #pragma unroll 1
-      for (int t = it.tb, te = it.te; t < te; ++t) {
+      for (int t = it.tb + (solo ? half : 0), te = it.te, by = solo ? 2 : 1; t < te; t += by) {
         if (!waits(&sm.s_full[half], ntile & 1)) return;
         ++ntile;
         __syncwarp();
@@ -252,31 +260,26 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
     }
     kv += it.te > it.tb ? it.te - it.tb + 1 : 0;
 
-    // the next item's Q goes in before this one's output goes out
+    // The next item's Q goes in before this one's output goes out: every score that reads Q is
+    // done (of a solo unit only once half 1 has handed its part over, see below).
     const uint32_t nx = idx + 1;
     if (!waits(&sm.item_full[nx % kItems], (nx / kItems) & 1)) return;
     const TcItem& next = sm.items[nx % kItems];
-    if (next.valid && active(next)) {  // every score of this item is done, so Q is free
-      load_q<D>(a, next, half, sm.q[half], wt);
-      mbar_arrive(&sm.q_full[half]);
-    }
+    if (!solo) next_q(next);
     if (on) {
       if (!waits(&sm.o_full[half], nitem & 1)) return;
       ++nitem;
       tc_fence_after();
     }
+    const bool joined = solo && it.active(1);
+    constexpr int kPass = D / 2;  // columns that half 1 hands over at a time
+    float* hand = reinterpret_cast<float*>(sm.q[1]) + wt * kPass;  // 16-byte pieces, spread over the banks
     const bool bad = *reinterpret_cast<volatile int*>(&sm.bad[idx % kItems]) != 0;
-    const bool mine = row < it.rows;
-    const int tok = it.q0 + row / g, head = it.h * g + row % g;
-    const size_t at = (size_t)tok * a.Hq + head;
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const size_t part = (size_t)it.slot * kTcM + half * 128 + wt;
-    if (mine) {
-      if (!it.whole)
-        a.part_ml[part] = make_float2(m * sl, l);
-      else if (a.lse)
-        a.lse[at] = lse_of(m * sl, l);
-    }
+    const bool mine = row < it.rows && (half == 0 || !solo);
+    const int qt = a.s.by_g.div(row);
+    const size_t at = (size_t)(it.q0 + qt) * a.Hq + it.h * g + (row - qt * g);
+    const size_t part = (size_t)it.slot * kTcM + (solo ? 0 : half * 128) + wt;
+    float f0 = 1.f, f1 = 0.f;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t o[32];
@@ -287,10 +290,10 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0;
       }
-      if (mine && bad) {
+      if (row < it.rows && on && bad) {
         const __nv_bfloat16* vc = reinterpret_cast<const __nv_bfloat16*>(a.vc);
         const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
-        for (int t = it.tb; t < it.te; ++t) {
+        for (int t = it.tb + (solo ? half : 0); t < it.te; t += solo ? 2 : 1) {
           if (!edge_tile<kTcBN>(t, pos_first, pos_last, window)) continue;
           for (int j = t * kTcBN; j < (t + 1) * kTcBN; ++j) {
             if (j > pos || (window > 0 && j <= pos - window)) continue;
@@ -305,7 +308,47 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
           }
         }
       }
+      __syncwarp();
+      const int c0 = c % kPass / 4;  // first 16-byte piece of these columns
+      if (joined && half == 1) {
+        if (c % kPass == 0 && !waits(&sm.sum_empty, (nsum & 1) ^ 1)) return;
+        if (c == 0) sm.ml[wt] = make_float2(m, l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(hand + ((c0 + e) ^ (wt & 7)) * 4) =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        if ((c + 32) % kPass == 0) {
+          mbar_arrive(&sm.sum_full);
+          ++nsum;
+        }
+        continue;
+      }
+      if (joined) {
+        if (c % kPass == 0 && !waits(&sm.sum_full, nsum & 1)) return;
+        if (c == 0) {  // both parts on the larger maximum
+          const float2 y = sm.ml[wt];
+          const float top = fmaxf(m, y.x), safe = top == -INFINITY ? 0.f : top;
+          f0 = ex2((m - safe) * sl);
+          f1 = ex2((y.x - safe) * sl);
+          l = l * f0 + y.y * f1;
+          m = top;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 y = *reinterpret_cast<const float4*>(hand + ((c0 + e) ^ (wt & 7)) * 4);
+          o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) * f0 + y.x * f1);
+          o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) * f0 + y.y * f1);
+          o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) * f0 + y.z * f1);
+          o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) * f0 + y.w * f1);
+        }
+        if ((c + 32) % kPass == 0) {
+          mbar_arrive(&sm.sum_empty);
+          ++nsum;
+        }
+      }
       if (mine && it.whole) {
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        if (c == 0 && a.lse) a.lse[at] = lse_of(m * sl, l);
         uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -316,6 +359,7 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
                               pack_bf16(x[6], x[7]));
         }
       } else if (mine) {
+        if (c == 0) a.part_ml[part] = make_float2(m * sl, l);
         uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * D + c);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -323,68 +367,141 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
       }
       __syncwarp();
     }
+    if (solo) {
+      // Q of half 0 was read by half 1's scores too, and half 1's part lay in its own Q
+      if (joined && half == 1 && !waits(&sm.sum_empty, (nsum & 1) ^ 1)) return;
+      next_q(next);
+    }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.item_empty[idx % kItems]);
   }
 }
 
-// One thread: every MMA of the CTA.
+// MMAs and commits by the elected lane of a warp whose lanes all take the same way: the
+// operands stay in uniform registers.  (Issued by one thread of a diverged warp, each MMA
+// costs moves into them, and the issue, not the tensor cores, sets the pace.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t e, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %0, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(e),
+      "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t e, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 e, %0, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(e),
+      "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t e, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %0, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(e),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+// One warp: every MMA of the CTA.
 template <int D>
-__device__ void run_mma(TcSmem<D>& sm, uint32_t tmem) {
+__device__ void run_mma(TcSmem<D>& sm) {
   using S = TcSmem<D>;
   constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
   volatile int* abort_flag = &sm.abort_flag;
+  const uint32_t e = elect_one();
   uint32_t kv = 0, nitem[2] = {0, 0}, np[2] = {0, 0};
-  auto wait_stage = [&](uint32_t st) {
-    return wait_in(&sm.full[st % S::kStages], (st / S::kStages) & 1, abort_flag);
-  };
-  auto scores = [&](uint32_t st, int half) {
-    const uint64_t q = smem_desc(smem_u32(sm.q[half]), 16, 1024);
+  auto waits = [&](uint64_t* bar, uint32_t parity) { return warp_waits(bar, parity, abort_flag); };
+  auto wait_stage = [&](uint32_t st) { return waits(&sm.full[st % S::kStages], (st / S::kStages) & 1); };
+  auto scores = [&](uint32_t st, int half, int q_half) {
+    const uint64_t q = smem_desc(smem_u32(sm.q[q_half]), 16, 1024);
     const uint64_t k = smem_desc(smem_u32(sm.k[st % S::kStages]), 16, kGroupBytes<D>);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
-      mma_bf16(tmem + half * 128, q + (i >> 2) * (S::kPanel >> 4) + kStepK * (i & 3),
-               k + (i >> 2) * (1024 >> 4) + kStepK * (i & 3), id_s, i > 0);
-    mma_commit(&sm.s_full[half]);
+      mma_ss(e, tmem + half * 128, q + (i >> 2) * (S::kPanel >> 4) + kStepK * (i & 3),
+             k + (i >> 2) * (1024 >> 4) + kStepK * (i & 3), id_s, i > 0);
+    commit_by(e, &sm.s_full[half]);
   };
   auto values = [&](uint32_t st, int half, bool first) {
     const uint64_t b = smem_desc(smem_u32(sm.v[st % S::kStages]), 1024, kGroupBytes<D>);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      mma_bf16_ta(tmem + 256 + half * 128, tmem + half * 128 + 8 * i, b + (2 * kGroupBytes<D> >> 4) * i, id_o,
-                  !first || i > 0);
+      mma_ts(e, tmem + 256 + half * 128, tmem + half * 128 + 8 * i, b + (2 * kGroupBytes<D> >> 4) * i, id_o,
+             !first || i > 0);
   };
   for (uint32_t idx = 0;; ++idx) {
-    if (!wait_in(&sm.item_full[idx % kItems], (idx / kItems) & 1, abort_flag)) return;
+    if (!waits(&sm.item_full[idx % kItems], (idx / kItems) & 1)) return;
     const TcItem& it = sm.items[idx % kItems];
     if (!it.valid) return;
     const int tiles = it.te - it.tb;
-    const int halves = it.rows - it.blk * kTcM > 128 ? 2 : 1;
-    mbar_arrive(&sm.item_empty[idx % kItems]);
+    const bool solo = it.solo();
+    __syncwarp();
+    if (e) mbar_arrive(&sm.item_empty[idx % kItems]);
     if (tiles == 0) continue;
     if (!wait_stage(kv)) return;
-    for (int h = 0; h < halves; ++h) {
-      if (!wait_in(&sm.q_full[h], nitem[h] & 1, abort_flag)) return;
-      ++nitem[h];
-      tc_fence_after();
-      scores(kv, h);
-    }
-    mma_commit(&sm.empty[kv % S::kStages]);
-    ++kv;
-    for (int j = 0; j < tiles; ++j, ++kv) {
-      if (!wait_stage(kv)) return;
-      for (int h = 0; h < halves; ++h) {
-        if (!wait_in(&sm.p_full[h], np[h] & 1, abort_flag)) return;
-        ++np[h];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (h == 0 || !solo) {
+        if (!waits(&sm.q_full[h], nitem[h] & 1)) return;
+        ++nitem[h];
         tc_fence_after();
-        values(kv, h, j == 0);
-        if (j + 1 < tiles)
-          scores(kv, h);
-        else
-          mma_commit(&sm.o_full[h]);
+        scores(kv, h, h);
       }
-      mma_commit(&sm.empty[kv % S::kStages]);
+    commit_by(e, &sm.empty[kv % S::kStages]);
+    ++kv;
+    if (solo) {
+      // halves take turns: P_h V of tile j, then half h's scores of tile j + 2
+      if (!wait_stage(kv)) return;
+      tc_fence_after();
+      if (tiles > 1) scores(kv, 1, 0);
+      for (int j0 = 0; j0 < tiles; j0 += 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = j0 + h;
+          if (j < tiles) {
+            if (!wait_stage(kv) || !waits(&sm.p_full[h], np[h] & 1)) return;
+            ++np[h];
+            tc_fence_after();
+            values(kv, h, j < 2);
+            commit_by(e, &sm.empty[kv % S::kStages]);
+            if (j + 2 < tiles) {
+              if (!wait_stage(kv + 1)) return;
+              tc_fence_after();
+              scores(kv + 1, h, 0);
+            } else {
+              commit_by(e, &sm.o_full[h]);
+            }
+            ++kv;
+          }
+        }
+      }
+    } else {
+      for (int j = 0; j < tiles; ++j, ++kv) {
+        if (!wait_stage(kv)) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!waits(&sm.p_full[h], np[h] & 1)) return;
+          ++np[h];
+          tc_fence_after();
+          values(kv, h, j == 0);
+          if (j + 1 < tiles)
+            scores(kv, h, h);
+          else
+            commit_by(e, &sm.o_full[h]);
+        }
+        commit_by(e, &sm.empty[kv % S::kStages]);
+      }
     }
   }
 }
@@ -447,6 +564,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
       mbar_init(&sm.q_full[h], 128);
       mbar_init(&sm.o_full[h], 1);
     }
+    mbar_init(&sm.sum_full, 128);
+    mbar_init(&sm.sum_empty, 128);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
       mbar_init(&sm.item_empty[i], 9);  // eight softmax warps and the MMA thread
@@ -469,7 +588,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 8) {
-      if ((tid & 31) == 0) run_mma<D>(sm, tmem);
+      run_mma<D>(sm);
     } else if (warp == 9) {
       run_loads<D>(sm, a, sched, &mk, &mv, box);
     }

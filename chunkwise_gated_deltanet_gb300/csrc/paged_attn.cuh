@@ -25,14 +25,13 @@ struct AttnArgs {
   SchedArgs s;
 };
 
-// The kernel for few rows (bf16, d = 64 or 128): 16 mt rows a unit, mt = 1 or 2.
-int paged_mma_grid();
-size_t paged_mma_part_bytes(int mt, int d);
-int paged_mma_requests();  // requests a launch takes
-cudaError_t launch_paged_mma(AttnArgs a, int mt, int d, cudaStream_t stream);
+// The kernel for few rows (bf16, d = 64 or 128), 16 a unit: partial-result bytes, the
+// requests a launch takes, and the launch (a.part_o set).
+size_t paged_mma_part_bytes(int d);
+int paged_mma_requests();
+cudaError_t launch_paged_mma(AttnArgs a, int d, cudaStream_t stream);
 
-// The tensor-core kernel for chunks of new tokens (bf16, d = 64 or 128): partial-result
-// bytes for a grid, and its launch (a.part_o set; a.part_ml is placed behind it).
+// The same of the tensor-core kernel for chunks of new tokens (bf16, d = 64 or 128).
 size_t paged_tc_part_bytes(int grid, int d);
 int paged_tc_requests();
 cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream);

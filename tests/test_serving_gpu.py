@@ -453,3 +453,57 @@ def test_step_continues_the_chunk_forward():
     out = gdn.recurrent_step(*(x[70:] for x in d), pd, index.to(DEV), _i32([0, 5]))
     assert (out - full[0, 70:]).abs().max() <= 1e-4 * full.abs().max()
     assert (pd[int(index[0])] - Sf[0]).abs().max() <= 1e-4 * Sf.abs().max()
+
+
+@pytest.mark.parametrize("d,ql,kv", [(128, 9, 9001), (64, 7, 5000), (128, 32, 129), (128, 5, 128), (64, 20, 2500)])
+def test_attention_units_of_up_to_128_rows(d, ql, kv):
+    """17 to 128 rows a key/value head: both halves of the tensor-core kernel take the same
+    rows, over one tile, a few, and a split axis."""
+    lens = [kv, 300, ql]
+    res = _attend([ql, 6, ql], lens, 4, 1, d, 16, "bf16", seed=ql)
+    _check_attend(res, d, lens, True)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attention_masked_tokens_in_small_units(bad):
+    """The same as for whole row blocks: a bad value of a late token, 36 rows over 3 tiles."""
+    ql, kv = 9, 300
+
+    def edit(n, k, v):
+        v[kv - 4, :, 7] = bad
+    o, z, (ro, rz, A, X) = _attend([ql], [kv], 4, 1, 128, 16, "bf16", edit=edit, seed=2)[0]
+    sees = kv - ql + torch.arange(ql) >= kv - 4
+    assert not torch.isfinite(o[sees][:, :, 7]).any()
+    part = lambda x: x[~sees]  # noqa: E731
+    _check_attend([(part(o), part(z), tuple(part(x) for x in (ro, rz, A, X)))], 128, [kv], True)
+    cols = [c for c in range(128) if c != 7]
+    to, _ = R.bounds(ro, rz, A, X, 128, kv, True)
+    assert ((o - ro).abs() <= to)[:, :, cols].all()
+
+
+def test_attention_caches_beyond_l2():
+    """Keys and values that pass half of L2, several waves of row blocks: a sample of rows."""
+    ql, kv, Hq, Hkv, d, block = [1300, 700], [17000, 9000], 64, 8, 128, 32
+    g = torch.Generator(device=DEV).manual_seed(0)
+    held = [-(-x // block) for x in kv]
+    nb = sum(held)
+    ids = torch.randperm(nb, generator=g, device=DEV).to(torch.int32)
+    tables = torch.full((2, max(held)), -1, dtype=torch.int32, device=DEV)
+    tables[0, :held[0]], tables[1, :held[1]] = ids[:held[0]], ids[held[0]:]
+    kc, vc = (torch.randn(nb, block, Hkv, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(sum(ql), Hq, d, generator=g, device=DEV).to(torch.bfloat16)
+    cu = np.concatenate([[0], np.cumsum(ql)])
+    out, lse = gdn.paged_attention(q, kc, vc, tables, _i32(kv), _i32(cu), max(ql), return_lse=True)
+    gdn.gdn_check_status()
+    r = np.random.RandomState(0)
+    for n in range(2):
+        k = kc[tables[n, :held[n]].long()].flatten(0, 1)[:kv[n]]
+        v = vc[tables[n, :held[n]].long()].flatten(0, 1)[:kv[n]]
+        rows = sorted(set(r.randint(0, ql[n], 40)) | {0, ql[n] - 1})
+        for i in rows:
+            h = int(r.randint(Hq))
+            p = kv[n] - ql[n] + i
+            kk, vv = k[:p + 1, h * Hkv // Hq][:, None], v[:p + 1, h * Hkv // Hq][:, None]
+            ref = R.attention(q[cu[n] + i, h][None, None], kk, vv, p, d ** -0.5, 0)
+            got = (out[cu[n] + i, h].double().cpu()[None, None], lse[cu[n] + i, h].double().cpu()[None, None], ref)
+            _check_attend([got], d, [kv[n]], True, f"token {i} head {h}")
