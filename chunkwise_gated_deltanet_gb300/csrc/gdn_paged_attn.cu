@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
         for (int b = 0; b < NC / CV; ++b)
 #pragma unroll
           for (int c = 0; c < CV; ++c)
-            a.part_o[at * D + b * 16 * CV + tx * CV + c] = o[i][b * CV + c];
+            a.part_o[part_at<D, M>(it.slot, rr, (b * 16 * CV + tx * CV + c) & ~3) + (tx * CV + c) % 4] = o[i][b * CV + c];
       }
     }
   }
@@ -283,6 +283,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.by_g = FastDiv((unsigned)k.s.g); k.s.Hkv = a.Hkv; k.s.window = a.window;
   k.s.max_blocks = a.max_blocks; k.s.max_kv = (long long)a.max_blocks * a.block_size;
   k.s.min_tiles = 1;
+  k.s.unit_cost = 1;
   k.part_o = reinterpret_cast<float*>(a.workspace);
   auto ranges = [&](int most, int rows_lo, int rows_hi, auto launch) {
     k.s.rows_lo = rows_lo;

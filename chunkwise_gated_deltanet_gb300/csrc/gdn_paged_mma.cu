@@ -292,7 +292,7 @@ __device__ void run_rows(MmSmem<D>& sm, const AttnArgs& a) {
         } else {
           const size_t at = (size_t)it.slot * M + rr;
           if (c0 == 0 && c == 0) a.part_ml[at] = make_float2(top * sl, sum);
-          st4(a.part_o + at * D + c0 + c, x[0], x[1], x[2], x[3]);
+          st4(a.part_o + part_at<D, M>(it.slot, rr, c0 + c), x[0], x[1], x[2], x[3]);
         }
       }
       named_sync(1, 32 * kMmWarps);
@@ -419,6 +419,7 @@ cudaError_t launch_mma(AttnArgs a, cudaStream_t stream) {
       !make_page_map(&mv, a.vc, a.num_blocks, a.bs, a.s.Hkv, D, box))
     return cudaErrorInvalidValue;
   const int grid = mma_grid();
+  a.s.unit_cost = 2;  // a unit's start and join take about as long as two tiles
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kMmM * D);
   paged_mma_kernel<D><<<grid, kMmThreads, bytes, stream>>>(a, mk, mv, box, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -40,8 +40,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kTcM = 256, kTcBN = 128, kTcThreads = 384, kItems = 4;
-using TcSched = Sched<kTcM, kTcBN, 1024, true>;
+constexpr int kTcM = 256, kTcBN = 128, kTcThreads = 384, kItems = 4, kTcRequests = 512;
+using TcSched = Sched<kTcM, kTcBN, kTcRequests, true>;
 
 struct TcItem {
   int valid, n, h, blk, q0, ql, kl, rows, tb, te, whole, slot;
@@ -69,6 +69,7 @@ struct TcSmem {
   int abort_flag;
   int bad[kItems];  // a value that some row does not see is not finite
   float2 ml[128];   // half 1's maxima and sums of a solo unit
+  uint8_t out[8][32 * 80];  // a softmax warp's 32 rows of 32 output columns, 16 bytes of padding each
 };
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -280,6 +281,19 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
     const size_t at = (size_t)(it.q0 + qt) * a.Hq + it.h * g + (row - qt * g);
     const size_t part = (size_t)it.slot * kTcM + (solo ? 0 : half * 128) + wt;
     float f0 = 1.f, f1 = 0.f;
+    // Outputs leave as 64-byte pieces of rows, four lanes each, through shared memory: lane's
+    // rows are lane / 4 + 8 i of the warp's 32 (from a thread's own row, a store would touch 32
+    // lines).
+    uint8_t* stage = sm.out[half * 4 + warp];
+    size_t out_row[4];
+    if (it.whole) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r2 = row - lane + 8 * i + (lane >> 2), t2 = a.s.by_g.div(r2);
+        out_row[i] = ((size_t)(it.q0 + t2) * a.Hq + it.h * g + (r2 - t2 * g)) * D + (lane & 3) * 8;
+        if (r2 >= it.rows || (solo && half == 1)) out_row[i] = ~(size_t)0;
+      }
+    }
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t o[32];
@@ -346,24 +360,29 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
           ++nsum;
         }
       }
-      if (mine && it.whole) {
+      if (it.whole) {
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        if (c == 0 && a.lse) a.lse[at] = lse_of(m * sl, l);
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + c);
+        if (c == 0 && a.lse && mine) a.lse[at] = lse_of(m * sl, l);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[8 * e + i]) * inv;
-          dst[e] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                              pack_bf16(x[6], x[7]));
+          *reinterpret_cast<uint4*>(stage + lane * 80 + e * 16) = make_uint4(
+              pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (out_row[i] != ~(size_t)0)
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + out_row[i] + c) =
+                *reinterpret_cast<const uint4*>(stage + (8 * i + (lane >> 2)) * 80 + (lane & 3) * 16);
       } else if (mine) {
         if (c == 0) a.part_ml[part] = make_float2(m * sl, l);
-        uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * D + c);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          *reinterpret_cast<uint4*>(a.part_o + part_at<D, kTcM>(it.slot, (solo ? 0 : half * 128) + wt, c + 4 * e)) =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
       __syncwarp();
     }
@@ -631,11 +650,12 @@ cudaError_t launch_tc_d(const AttnArgs& a, int grid, cudaStream_t stream) {
 
 size_t paged_tc_part_bytes(int grid, int d) { return (size_t)2 * grid * kTcM * (d + 2) * 4; }
 
-int paged_tc_requests() { return 1024; }
+int paged_tc_requests() { return kTcRequests; }
 
 cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream) {
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kTcM * d);
   // whole units in waves when keys and values pass half of the L2 cache (129 MB)
+  a.s.unit_cost = 2;
   a.s.wave_tokens = (64LL << 20) / ((long long)a.s.Hkv * d * 4);
   return d == 128 ? launch_tc_d<128>(a, grid, stream) : launch_tc_d<64>(a, grid, stream);
 }

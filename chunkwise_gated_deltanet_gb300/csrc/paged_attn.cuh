@@ -17,7 +17,7 @@ struct AttnArgs {
   const void* vc;
   void* out;
   float* lse;      // may be null
-  float* part_o;   // [2 CTAs][M][D] unnormalised sums
+  float* part_o;   // [2 CTAs][D / 4][M][4] unnormalised sums (part_at)
   float2* part_ml; // [2 CTAs][M] running maximum (log2 units) and sum
   long long q_stride;
   int Hq, bs, num_blocks;
@@ -58,85 +58,125 @@ __device__ __forceinline__ void st_out(void* p, size_t i, float x) {
     reinterpret_cast<float*>(p)[i] = x;
 }
 
+template <bool BF16>
+__device__ __forceinline__ void st_out4(void* p, size_t i, float4 x) {
+  if (BF16) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p) + i) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = x;
+  }
+}
+
+// Place of columns c .. c + 3 (c % 4 == 0) of a row in part_o: a thread of the tensor-core kernel
+// has a whole row, so neighbouring rows' pieces are neighbours (row after row, a warp's store
+// would touch 32 lines).
+template <int D, int M>
+__device__ __forceinline__ size_t part_at(int slot, int row, int c) {
+  return (((size_t)slot * (D / 4) + c / 4) * M + row) * 4;
+}
+
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 // Joins the partial results of the units that share boundaries cut.  CTA (c - 1, y) looks at
 // the boundary between shares c - 1 and c; the CTAs of all boundaries inside one unit share
-// its rows.  A row of up to kJoinWarps parts takes a warp, one of more parts the whole CTA,
-// a warp for every kJoinWarps-th part.  The parts are summed in the order of the shares, the
+// its rows.  Two rows of up to kJoinWarps parts take a warp, of more parts the whole CTA, a
+// warp for every kJoinWarps-th part.  The parts are summed in the order of the shares, the
 // warps in theirs: the same sums every time.
 template <int D, typename SCHED, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
   constexpr int M = SCHED::kM;
-  constexpr int NL = (D + 31) / 32;  // columns a lane
   __shared__ typename SCHED::Mem mem;
-  __shared__ float acc_s[kJoinWarps][D], l_s[kJoinWarps];
+  __shared__ float4 acc_s[kJoinWarps][(D + 63) / 64][32];
+  __shared__ float l_s[kJoinWarps][32];
   SCHED sched;
   sched.template init<kJoinThreads>(a.s, &mem, 0, grid);
-  after_previous_kernel();
   const int c = blockIdx.x + 1;
   if (c >= sched.G) return;
   const long long b = sched.share(c);
   if (b >= sched.total) return;
   sched.locate(b);
-  const long long u0 = sched.unit0;
-  if (u0 == b) return;
-  int lo;
-  bool empty;
-  const long long u1 = u0 + sched.tiles(sched.r, sched.blk, &lo, &empty);
-  const int c0 = sched.share_of(u0), c1 = sched.share_of(u1 - 1);  // the shares that hold a part
+  const long long u0 = sched.unit0, u1 = u0 + sched.cost(sched.r, sched.blk);
+  if (b <= u0 + sched.s.unit_cost) return;  // cuts nothing: the unit is the later share's
+  int c0 = sched.share_of(u0);
+  while (sched.share(c0 + 1) <= u0 + sched.s.unit_cost) ++c0;
+  const int c1 = sched.share_of(u1 - 1);  // shares c0 .. c1 hold a part
   // part 0 is in slot0, part i in slot 2 (c0 + i)
   const int parts = c1 - c0 + 1, slot0 = 2 * c0 + (u0 > sched.share(c0) ? 1 : 0);
+  after_previous_kernel();
+  // A warp has a pair of rows, whose pieces of 16 bytes lie side by side: lane, row lane & 1 of
+  // the pair and columns 4 (lane / 2 + 16 j) .. + 3.
+  constexpr int NJ = (D + 63) / 64;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = min(sched.r.rows - sched.blk * M, M);
+  const int pairs = (min(sched.r.rows - sched.blk * M, M) + 1) / 2;
   const int me = (c - 1 - c0) * gridDim.y + blockIdx.y, team = (parts - 1) * gridDim.y;
   const bool whole_cta = parts > kJoinWarps;
-  const int row_step = whole_cta ? team : team * kJoinWarps;
-  for (int rr = whole_cta ? me : me * kJoinWarps + warp; rr < rows; rr += row_step) {
+  const int step = whole_cta ? team : team * kJoinWarps;
+  for (int pair = whole_cta ? me : me * kJoinWarps + warp; pair < pairs; pair += step) {
+    const int rr = 2 * pair + (lane & 1), row = sched.blk * M + rr;
     float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32)
+    for (int i = lane >> 1; i < parts; i += 16)
       m = fmaxf(m, a.part_ml[(size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * M + rr].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float safe = m == -INFINITY ? 0.f : m;
-    float acc[NL], l = 0.f;
+    float4 acc[NJ];
+    float l = 0.f;
 #pragma unroll
-    for (int j = 0; j < NL; ++j) acc[j] = 0.f;
+    for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = whole_cta ? warp : 0; i < parts; i += whole_cta ? kJoinWarps : 1) {
-      const size_t at = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * M + rr;
-      const float2 ml = a.part_ml[at];
+      const int slot = i == 0 ? slot0 : 2 * (c0 + i);
+      const float2 ml = a.part_ml[(size_t)slot * M + rr];
       const float w = exp2f(ml.x - safe);
       l = fmaf(w, ml.y, l);
 #pragma unroll
-      for (int j = 0; j < NL; ++j)
-        if (lane + 32 * j < D) acc[j] = fmaf(w, a.part_o[at * D + lane + 32 * j], acc[j]);
+      for (int j = 0; j < NJ; ++j) {
+        const int col = 4 * ((lane >> 1) + 16 * j);
+        if (col < D) {
+          const float4 y = *reinterpret_cast<const float4*>(a.part_o + part_at<D, M>(slot, rr, col));
+          acc[j].x = fmaf(w, y.x, acc[j].x);
+          acc[j].y = fmaf(w, y.y, acc[j].y);
+          acc[j].z = fmaf(w, y.z, acc[j].z);
+          acc[j].w = fmaf(w, y.w, acc[j].w);
+        }
+      }
     }
     if (whole_cta) {
 #pragma unroll
-      for (int j = 0; j < NL; ++j)
-        if (lane + 32 * j < D) acc_s[warp][lane + 32 * j] = acc[j];
-      if (lane == 0) l_s[warp] = l;
+      for (int j = 0; j < NJ; ++j) acc_s[warp][j][lane] = acc[j];
+      l_s[warp][lane] = l;
       __syncthreads();
       if (warp == 0) {
         for (int w = 1; w < kJoinWarps; ++w) {
-          l += l_s[w];
+          l += l_s[w][lane];
 #pragma unroll
-          for (int j = 0; j < NL; ++j)
-            if (lane + 32 * j < D) acc[j] += acc_s[w][lane + 32 * j];
+          for (int j = 0; j < NJ; ++j) {
+            const float4 y = acc_s[w][j][lane];
+            acc[j].x += y.x;
+            acc[j].y += y.y;
+            acc[j].z += y.z;
+            acc[j].w += y.w;
+          }
         }
       }
       __syncthreads();
       if (warp != 0) continue;
     }
-    const int row = sched.blk * M + rr, t = a.s.by_g.div(row);
+    if (row >= sched.r.rows) continue;
+    const int t = a.s.by_g.div(row);
     const size_t at = (size_t)(sched.r.q0 + t) * a.Hq + sched.h * a.s.g + (row - t * a.s.g);
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    if (a.lse && lane == 0) a.lse[at] = lse_of(m, l);
+    if (a.lse && lane < 2) a.lse[at] = lse_of(m, l);
 #pragma unroll
-    for (int j = 0; j < NL; ++j)
-      if (lane + 32 * j < D) st_out<BF16>(a.out, at * D + lane + 32 * j, acc[j] * inv);
+    for (int j = 0; j < NJ; ++j) {
+      const int col = 4 * ((lane >> 1) + 16 * j);
+      if (col < D)
+        st_out4<BF16>(a.out, at * D + col,
+                      make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+    }
   }
 }
 
@@ -149,7 +189,7 @@ cudaError_t launch_join(const AttnArgs& a, bool bf16, int grid, cudaStream_t str
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid - 1, std::max(1, SCHED::kM / 32));
+  cfg.gridDim = dim3(grid - 1, std::max(1, SCHED::kM / 64));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &early;

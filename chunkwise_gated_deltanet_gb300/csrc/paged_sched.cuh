@@ -9,7 +9,8 @@
 // (unnormalised sums with their running maximum and sum), which the combine kernel joins in
 // the order of the shares, so results do not depend on timing.  A share has at most two
 // partial results: the unit that its start cuts (slot 0) and the one that its end cuts
-// (slot 1).
+// (slot 1).  A unit counts unit_cost tiles more than it has, for what it costs apart from its
+// tiles (queries in, results out); a boundary within these comes before the unit instead.
 //
 // With WAVES, a launch whose caches do not fit L2 first gives out whole units in waves, unit
 // w * CTAs + c to CTA c (odd waves the other way round), and shares only the last one to two
@@ -47,6 +48,7 @@ struct SchedArgs {
   FastDiv by_g;
   long long max_kv;           // max_blocks * block_size
   int rows_lo, rows_hi;       // requests with rows in (rows_lo, rows_hi] only
+  int unit_cost;              // what a unit costs apart from its tiles, in tiles
   int min_tiles;              // tiles a CTA takes at least (while there are that many)
   long long wave_tokens;      // WAVES: cached tokens (all heads) above which waves are used
 };
@@ -113,6 +115,12 @@ struct Sched {
     *lo = *empty ? 0 : l / BN;
     return *empty ? 1 : (hi + BN - 1) / BN - *lo;
   }
+  // What row block `b` counts on the line that the CTAs share.
+  __device__ __forceinline__ int cost(const Req& q, int b) const {
+    int l;
+    bool e;
+    return tiles(q, b, &l, &e) + s.unit_cost;
+  }
   __device__ __forceinline__ static int blocks(const Req& q) { return (q.rows + M - 1) / M; }
 
   // Whole CTA of NT threads: prefix sums of the requests' tiles and units into `m`.
@@ -129,9 +137,7 @@ struct Sched {
       if (n0 + tid < s.nn) {
         const Req q = load_req(s, n0 + tid);
         const int nb = blocks(q);
-        int lo;
-        bool e;
-        for (int b = 0; b < nb; ++b) x += tiles(q, b, &lo, &e);
+        for (int b = 0; b < nb; ++b) x += cost(q, b);
         x *= s.Hkv;
         u = nb * s.Hkv;
         if (WAVES && nb) tokens += q.kl;
@@ -198,7 +204,7 @@ struct Sched {
       // share c: what CTA c's waves leave of an even part, one tile at least
       long long x = 0;
       if (tid < G) {
-        for (int w = 0; w < waves; ++w) x += unit_tiles(wave_unit(w, tid));
+        for (int w = 0; w < waves; ++w) x += unit_cost_of(wave_unit(w, tid));
         x = max((total + G - 1) / G - x, 1LL);
       }
       long long inc = x;
@@ -236,13 +242,10 @@ struct Sched {
   }
 
   __device__ __forceinline__ int wave_unit(int w, int c) const { return w * G + (w & 1 ? G - 1 - c : c); }
-  // Tiles of unit `u`.
-  __device__ int unit_tiles(int u) const {
+  __device__ int unit_cost_of(int u) const {
     const int q = last_upto(mem->units, s.nn, u);
     const Req a = load_req(s, q);
-    int l;
-    bool e;
-    return tiles(a, (u - mem->units[q]) % blocks(a), &l, &e);
+    return cost(a, (u - mem->units[q]) % blocks(a));
   }
   // Last of the first n entries of an ascending array that is at most x.
   template <typename V>
@@ -257,14 +260,10 @@ struct Sched {
     }
     return lo;
   }
-  // Tiles of row blocks 0 .. upto - 1 of request r, by a whole warp.
-  __device__ int tiles_before(int upto) const {
+  // Cost of row blocks 0 .. upto - 1 of request r, by a whole warp.
+  __device__ int cost_before(int upto) const {
     int sum = 0;
-    for (int b = threadIdx.x & 31; b < upto; b += 32) {
-      int l;
-      bool e;
-      sum += tiles(r, b, &l, &e);
-    }
+    for (int b = threadIdx.x & 31; b < upto; b += 32) sum += cost(r, b);
     return __reduce_add_sync(0xffffffffu, sum);
   }
 
@@ -275,7 +274,7 @@ struct Sched {
     const int left = u - mem->units[n], nb = blocks(r);
     h = left / nb;
     blk = left - h * nb;
-    unit0 = mem->pre[n] + (mem->pre[n + 1] - mem->pre[n]) / s.Hkv * h + tiles_before(blk);
+    unit0 = mem->pre[n] + (mem->pre[n + 1] - mem->pre[n]) / s.Hkv * h + cost_before(blk);
   }
 
   // Request, head, row block and start of the unit that holds tile `x`; whole warps.
@@ -289,9 +288,8 @@ struct Sched {
     // 32 row blocks at a time: the first whose inclusive sum passes what is left
     const int nb = blocks(r), lane = threadIdx.x & 31;
     for (int b0 = 0;; b0 += 32) {
-      int l, c = 0;
-      bool e;
-      if (b0 + lane < nb) c = tiles(r, b0 + lane, &l, &e);
+      int c = 0;
+      if (b0 + lane < nb) c = cost(r, b0 + lane);
       int inc = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -327,11 +325,19 @@ struct Sched {
       it->slot = 0;
       return true;
     }
-    if (pos >= end) return false;
-    if (!started) {
-      locate(pos);
+    if (!started) {  // boundaries within a unit's own cost come before it
+      if (pos < total) {
+        if (end < total) {
+          locate(end);
+          if (end <= unit0 + s.unit_cost) end = unit0;
+        }
+        locate(pos);
+        if (pos <= unit0 + s.unit_cost) pos = first = unit0;
+      }
       started = true;
+      if (pos >= end) return false;
     } else {
+      if (pos >= end) return false;
       if (++blk == blocks(r)) {
         blk = 0;
         if (++h == s.Hkv) {
@@ -345,14 +351,14 @@ struct Sched {
     }
     int lo;
     bool empty;
-    const int c = tiles(r, blk, &lo, &empty);
+    const int c = tiles(r, blk, &lo, &empty) + s.unit_cost;
     const long long stop = min(unit0 + c, end);
     it->n = n;
     it->h = h;
     it->blk = blk;
     it->r = r;
-    it->tb = empty ? 0 : lo + (int)(pos - unit0);
-    it->te = empty ? 0 : lo + (int)(stop - unit0);
+    it->tb = empty || pos == unit0 ? lo : lo + (int)(pos - unit0) - s.unit_cost;
+    it->te = empty ? 0 : lo + (int)(stop - unit0) - s.unit_cost;
     it->whole = pos == unit0 && stop == unit0 + c;
     it->slot = 2 * cta + (unit0 > first ? 1 : 0);
     pos = stop;
