@@ -240,17 +240,21 @@ __device__ void run_softmax(TcSmem<D>& sm, const AttnArgs& a, uint32_t tmem, int
           // values of this tile become zeros here and are added at the end, row by row
           const uint32_t st = kv + (t - it.tb) + 1, slot = st % TcSmem<D>::kStages;
           if (!waits(&sm.full[slot], (st / TcSmem<D>::kStages) & 1)) return;
-#pragma unroll
+          uint32_t big = 0;  // the largest magnitudes, of even and odd columns
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(
+            const uint4 x = *reinterpret_cast<const uint4*>(
                 sm.v[slot] + tile_offset<D>(wt, (c >> 3) * 64 + ((c + wt) & 7) * 8));
-            const uint4 x = *at;
-            if (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w)) {
-              uint16_t* e = reinterpret_cast<uint16_t*>(at);
-              for (int i = 0; i < 8; ++i)
-                if ((e[i] & 0x7f80u) == 0x7f80u) e[i] = 0;
-              if (t * kTcBN + wt < it.kl) *reinterpret_cast<volatile int*>(&sm.bad[idx % kItems]) = 1;
+            big = __vmaxu2(__vmaxu2(big, x.x & 0x7fff7fffu), __vmaxu2(x.y & 0x7fff7fffu, x.z & 0x7fff7fffu));
+            big = __vmaxu2(big, x.w & 0x7fff7fffu);
+          }
+          if (not_finite(big)) {
+#pragma unroll 1
+            for (int c = 0; c < D; ++c) {
+              volatile uint16_t* e = reinterpret_cast<uint16_t*>(sm.v[slot] + tile_offset<D>(wt, c));
+              if ((*e & 0x7f80u) == 0x7f80u) *e = 0;
             }
+            if (t * kTcBN + wt < it.kl) *reinterpret_cast<volatile int*>(&sm.bad[idx % kItems]) = 1;
           }
           fence_async_smem();
         }

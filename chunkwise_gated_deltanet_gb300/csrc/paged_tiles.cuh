@@ -14,6 +14,7 @@ template <int BN>
 __device__ __forceinline__ bool edge_tile(int t, int pos_first, int pos_last, int window) {
   return t * BN + BN - 1 > pos_first || (window > 0 && t * BN <= pos_last - window);
 }
+// Whether one of two bf16 (or of the largest magnitudes of two sets) is infinite or NaN.
 __device__ __forceinline__ bool not_finite(uint32_t two) {
   return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
 }
