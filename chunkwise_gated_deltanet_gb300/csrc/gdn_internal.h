@@ -208,10 +208,12 @@ struct PagedAttnArgs {
   void* workspace;
   long long q_stride;
   int N, T, Hq, Hkv, d, max_blocks, num_blocks, block_size;
-  int max_q_len, window;
+  int max_q_len, max_seq_len, window;  // max_seq_len 0: not known
   float scale;
   int bf16;
 };
+// Whether a request within the call's bounds has fewer than 2^31 tiles of work.
+bool paged_attn_fits(const PagedAttnArgs& a);
 size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_len);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
 

@@ -272,6 +272,22 @@ size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_le
   return std::max(paged_mma_part_bytes(d), p.tc ? paged_tc_part_bytes(grid, d) : 0);
 }
 
+// The most that one request can cost on the line that the CTAs share, by the host's bounds.
+constexpr double kMostCost = 2e9;
+double request_cost(const PagedAttnArgs& a, int M, int BN, int rows_hi) {
+  const long long room = (long long)a.max_blocks * a.block_size;
+  const long long kv = a.max_seq_len > 0 ? std::min<long long>(a.max_seq_len, room) : room;
+  const long long rows = std::min<long long>(std::min(std::max(a.max_q_len, 1), a.T) * (long long)(a.Hq / a.Hkv), rows_hi);
+  return double((rows + M - 1) / M) * a.Hkv * double(kv / BN + 8);
+}
+
+bool paged_attn_fits(const PagedAttnArgs& a) {
+  constexpr int kAll = 0x7fffffff;
+  const Plan p = plan_of(a.bf16, a.d, (long long)a.max_q_len * (a.Hq / a.Hkv));
+  if (p.simt) return request_cost(a, p.simt, kBN, kAll) <= kMostCost;
+  return request_cost(a, p.tc ? 256 : 16, p.tc ? 128 : 64, kAll) <= kMostCost;
+}
+
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
   const Plan p = plan_of(a.bf16, a.d, (long long)a.max_q_len * (a.Hq / a.Hkv));
@@ -280,14 +296,18 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   k.q = a.q; k.kc = a.k_cache; k.vc = a.v_cache; k.out = a.out; k.lse = a.lse;
   k.q_stride = a.q_stride; k.Hq = a.Hq; k.bs = a.block_size; k.num_blocks = a.num_blocks;
   k.scale_log2 = a.scale * 1.4426950408889634f;
-  k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.by_g = FastDiv((unsigned)k.s.g); k.s.Hkv = a.Hkv; k.s.window = a.window;
+  k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.by_g = FastDiv((unsigned)k.s.g);
+  k.s.by_hkv = FastDiv((unsigned)a.Hkv); k.s.Hkv = a.Hkv; k.s.window = a.window;
   k.s.max_blocks = a.max_blocks; k.s.max_kv = (long long)a.max_blocks * a.block_size;
   k.s.min_tiles = 1;
   k.s.unit_cost = 1;
   k.part_o = reinterpret_cast<float*>(a.workspace);
-  auto ranges = [&](int most, int rows_lo, int rows_hi, auto launch) {
+  // Launches over ranges of requests, `most` at a time, and few enough that the costs of their
+  // units (M rows, BN tokens a tile, by the host's bounds on the lengths) stay below 2^31.
+  auto ranges = [&](int most, int M, int BN, int rows_lo, int rows_hi, auto launch) {
     k.s.rows_lo = rows_lo;
     k.s.rows_hi = rows_hi;
+    most = (int)std::max(1.0, std::min<double>(most, kMostCost / request_cost(a, M, BN, rows_hi)));
     for (int n0 = 0; n0 < a.N; n0 += most) {
       k.s.nn = std::min(a.N - n0, most);
       k.s.seq_lens = a.seq_lens + n0;
@@ -302,18 +322,18 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (p.simt) {
     k.part_ml = reinterpret_cast<float2*>(k.part_o + (size_t)2 * grid * p.simt * a.d);
-    return ranges(kSimtRequests, 0, kAll, [&] {
+    return ranges(kSimtRequests, p.simt, kBN, 0, kAll, [&] {
       return p.simt == 16 ? launch_simt_d<16>(k, a.d, a.bf16, grid, stream)
                           : launch_simt_d<64>(k, a.d, a.bf16, grid, stream);
     });
   }
   if (p.tc) {
     // a single request is taken whatever its length, so that nothing is left over
-    e = ranges(paged_tc_requests(), a.N > 1 ? 16 : 0, kAll,
+    e = ranges(paged_tc_requests(), 256, 128, a.N > 1 ? 16 : 0, kAll,
                [&] { return launch_paged_tc(k, a.d, grid, stream); });
     if (e != cudaSuccess || a.N == 1) return e;
   }
-  return ranges(paged_mma_requests(), 0, p.tc ? 16 : kAll,
+  return ranges(paged_mma_requests(), 16, 64, 0, p.tc ? 16 : kAll,
                 [&] { return launch_paged_mma(k, a.d, stream); });
 }
 

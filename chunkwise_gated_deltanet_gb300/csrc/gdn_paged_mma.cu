@@ -34,11 +34,11 @@ struct MmSmem {
   static constexpr int kStages = 81920 / kTile;
   static constexpr int kCols = 64;        // columns joined at a time
   static constexpr int kRow = kCols + 8;  // padded: rows fall into different banks
-  uint8_t kv[kStages][kTile];
-  uint8_t q[2][(D / 64) * kMmM * 128];
+  alignas(1024) uint8_t kv[kStages][kTile];
+  alignas(16) uint8_t q[2][(D / 64) * kMmM * 128];
   MmItem items[2];
   uint64_t item_full[2], item_empty[2];
-  float o[kMmWarps][kMmM][kRow];
+  alignas(16) float o[kMmWarps][kMmM][kRow];
   float2 ml[kMmWarps][kMmM];
   uint64_t full[kStages], empty[kStages];
   MmSched::Mem sched;

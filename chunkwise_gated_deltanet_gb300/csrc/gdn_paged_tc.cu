@@ -32,6 +32,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <stddef.h>
+
 #include <algorithm>
 #include <numeric>
 
@@ -55,7 +57,7 @@ struct TcSmem {
   static constexpr int kPanel = 128 * 128;             // 128 rows of 64 bf16
   static constexpr int kTile = kPanel * (D / 64);
   static constexpr int kStages = D == 128 ? 2 : 4;
-  uint8_t q[2][kTile];
+  alignas(1024) uint8_t q[2][kTile];
   // a stage has V of a tile and K of the next one, which the MMA thread uses together: one
   // wait and one release a tile (an item's first stage has K only, its last one V only)
   uint8_t v[kStages][kTile], k[kStages][kTile];
@@ -69,7 +71,7 @@ struct TcSmem {
   int abort_flag;
   int bad[kItems];  // a value that some row does not see is not finite
   float2 ml[128];   // half 1's maxima and sums of a solo unit
-  uint8_t out[8][32 * 80];  // a softmax warp's 32 rows of 32 output columns, 16 bytes of padding each
+  alignas(16) uint8_t out[8][32 * 80];  // a softmax warp's 32 rows of 32 output columns, 16 bytes of padding each
 };
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -571,6 +573,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, int box, int* status) {
   extern __shared__ uint8_t smem_raw[];
+  static_assert(offsetof(TcSmem<D>, out) % 16 == 0 && offsetof(TcSmem<D>, k) % 1024 == 0 &&
+                    offsetof(TcSmem<D>, full) % 8 == 0, "alignment");
   TcSmem<D>& sm = *reinterpret_cast<TcSmem<D>*>(
       smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5;

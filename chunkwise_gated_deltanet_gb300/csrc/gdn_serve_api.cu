@@ -174,7 +174,10 @@ int gdn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
   a.max_blocks = max_blocks; a.num_blocks = num_blocks; a.block_size = block_size;
   a.max_q_len = max_q_len; a.window = window; a.scale = scale;
   a.bf16 = qkv_dtype == GDN_BF16;
-  (void)max_seq_len;
+  a.max_seq_len = max_seq_len;
+  if (!gdn::paged_attn_fits(a))
+    return set_error(GDN_EINVAL, "%s: problem too large (max_q_len x longest sequence; give max_seq_len "
+                     "where the tables' room is not used)", fn);
   return launched(fn, gdn::launch_paged_attn(a, (cudaStream_t)stream));
 }
 

@@ -95,10 +95,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   sched.template init<kJoinThreads>(a.s, &mem, 0, grid);
   const int c = blockIdx.x + 1;
   if (c >= sched.G) return;
-  const long long b = sched.share(c);
+  const int b = sched.share(c);
   if (b >= sched.total) return;
   sched.locate(b);
-  const long long u0 = sched.unit0, u1 = u0 + sched.cost(sched.r, sched.blk);
+  const int u0 = sched.unit0, u1 = u0 + sched.cost(sched.r, sched.blk);
   if (b <= u0 + sched.s.unit_cost) return;  // cuts nothing: the unit is the later share's
   int c0 = sched.share_of(u0);
   while (sched.share(c0 + 1) <= u0 + sched.s.unit_cost) ++c0;

@@ -45,7 +45,7 @@ struct SchedArgs {
   const int32_t* cu_seqlens;
   const int32_t* block_tables;
   int nn, T, g, Hkv, window, max_blocks;
-  FastDiv by_g;
+  FastDiv by_g, by_hkv;
   long long max_kv;           // max_blocks * block_size
   int rows_lo, rows_hi;       // requests with rows in (rows_lo, rows_hi] only
   int unit_cost;              // what a unit costs apart from its tiles, in tiles
@@ -82,24 +82,28 @@ __device__ __forceinline__ Req load_req(const SchedArgs& s, int n) {
 
 constexpr int kBalance = 256;  // CTAs up to which shares make up for uneven waves
 
+// Sums stay below 2^31 (the host sees to that for lengths within its bounds); beyond, they
+// saturate and the last units are left out.
+__device__ __forceinline__ int add_sat(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+
 // Shared memory of a scheduler.
 template <int NMAX, bool WAVES>
 struct SchedMem {
-  long long pre[NMAX + 1];            // tiles before each request
-  long long warp[32];
-  int units[WAVES ? NMAX + 1 : 1];    // units before each request
+  int pre[NMAX + 1];                // cost before each request
+  int warp[32];
+  int units[WAVES ? NMAX + 1 : 1];  // units before each request
   int warp_u[WAVES ? 32 : 1];
-  long long bounds[WAVES ? kBalance + 1 : 1];  // first tiles of the shares after waves
+  int bounds[WAVES ? kBalance + 1 : 1];  // starts of the shares after waves
 };
 
 // M rows a unit, BN tokens a tile, NMAX requests a launch.
 template <int M, int BN, int NMAX, bool WAVES>
 struct Sched {
   using Mem = SchedMem<NMAX, WAVES>;
-  static constexpr int kM = M;
+  static constexpr int kM = M, kTile = BN;
   SchedArgs s;
   const Mem* mem;
-  long long total, base, quot, first, pos, end, unit0;
+  int total, base, quot, first, pos, end, unit0;
   int G, rem, cta, n, h, blk;
   int waves, wave;
   Req r;
@@ -123,31 +127,29 @@ struct Sched {
   }
   __device__ __forceinline__ static int blocks(const Req& q) { return (q.rows + M - 1) / M; }
 
-  // Whole CTA of NT threads: prefix sums of the requests' tiles and units into `m`.
+  // Whole CTA of NT threads: prefix sums of the requests' costs and units into `m`.
   template <int NT>
   __device__ void init(const SchedArgs& args, Mem* m, int cta_id, int grid) {
     s = args;
     mem = m;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long carry = 0, tokens = 0;
-    int carry_u = 0;
+    int carry = 0, carry_u = 0;
+    float tokens = 0.f;  // for a threshold only
     for (int n0 = 0; n0 < s.nn; n0 += NT) {
-      long long x = 0;
-      int u = 0;
+      int x = 0, u = 0;
       if (n0 + tid < s.nn) {
         const Req q = load_req(s, n0 + tid);
         const int nb = blocks(q);
-        for (int b = 0; b < nb; ++b) x += cost(q, b);
-        x *= s.Hkv;
+        for (int b = 0; b < nb; ++b) x = add_sat(x, cost(q, b));
+        x = (int)min((long long)x * s.Hkv, 0x7fffffffLL);
         u = nb * s.Hkv;
-        if (WAVES && nb) tokens += q.kl;
+        if (WAVES && nb) tokens += (float)q.kl;
       }
-      long long inc = x;
-      int inc_u = u;
+      int inc = x, inc_u = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc = add_sat(inc, y);
         if (WAVES) {
           const int yu = __shfl_up_sync(0xffffffffu, inc_u, o);
           if (lane >= o) inc_u += yu;
@@ -159,18 +161,19 @@ struct Sched {
         if (WAVES) m->warp_u[warp] = inc_u;
       }
       __syncthreads();
-      long long before = carry;
-      int before_u = carry_u;
+      int before = carry, before_u = carry_u;
       for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += m->warp[w];
-        carry += m->warp[w];
+        if (w < warp) before = add_sat(before, m->warp[w]);
+        carry = add_sat(carry, m->warp[w]);
         if (WAVES) {
           if (w < warp) before_u += m->warp_u[w];
           carry_u += m->warp_u[w];
         }
       }
+      // the exclusive sum: the lane below's inclusive one
+      const int ex = __shfl_up_sync(0xffffffffu, inc, 1);
       if (n0 + tid < s.nn) {
-        m->pre[n0 + tid] = before + inc - x;
+        m->pre[n0 + tid] = lane ? add_sat(before, ex) : before;
         if (WAVES) m->units[n0 + tid] = before_u + inc_u - u;
       }
     }
@@ -180,8 +183,7 @@ struct Sched {
     }
     __syncthreads();
     total = carry;
-    const long long want = (total + s.min_tiles - 1) / s.min_tiles;
-    G = (int)min((long long)grid, max(want, 1LL));
+    G = min(grid, max((total + s.min_tiles - 1) / s.min_tiles, 1));
     cta = cta_id;
     base = 0;
     waves = 0;
@@ -189,10 +191,10 @@ struct Sched {
       // cached tokens of the requests, over the CTA
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
-      if (lane == 0) m->warp[warp] = tokens;
+      if (lane == 0) m->warp[warp] = __float_as_int(tokens);
       __syncthreads();
-      tokens = 0;
-      for (int w = 0; w < NT / 32; ++w) tokens += m->warp[w];
+      tokens = 0.f;
+      for (int w = 0; w < NT / 32; ++w) tokens += __int_as_float(m->warp[w]);
       if (tokens > s.wave_tokens) waves = max(carry_u / G - 1, 0);
       if (waves > 0) {
         find_unit(waves * G);
@@ -202,27 +204,27 @@ struct Sched {
     balanced = WAVES && waves > 0 && G <= kBalance;
     if (balanced) {
       // share c: what CTA c's waves leave of an even part, one tile at least
-      long long x = 0;
+      int x = 0;
       if (tid < G) {
-        for (int w = 0; w < waves; ++w) x += unit_cost_of(wave_unit(w, tid));
-        x = max((total + G - 1) / G - x, 1LL);
+        for (int w = 0; w < waves; ++w) x = add_sat(x, unit_cost_of(wave_unit(w, tid)));
+        x = max(total / G + 1 - x, 1);
       }
-      long long inc = x;
+      int inc = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc = add_sat(inc, y);
       }
       __syncthreads();  // the sums of tokens have been read
       if (lane == 31) m->warp[warp] = inc;
       __syncthreads();
-      for (int w = 0; w < warp; ++w) inc += m->warp[w];
-      if (tid < G) m->bounds[tid] = min(total, base + inc - x);
-      if (tid == 0) m->bounds[G] = total;
+      for (int w = 0; w < warp; ++w) inc = add_sat(inc, m->warp[w]);
+      if (tid < G) m->bounds[tid + 1] = tid + 1 == G ? total : min(total, add_sat(base, inc));
+      if (tid == 0) m->bounds[0] = base;
       __syncthreads();
     }
     quot = (total - base) / G;
-    rem = (int)(total - base - quot * G);
+    rem = total - base - quot * G;
     wave = 0;
     first = cta < G ? share(cta) : total;
     pos = first;
@@ -230,15 +232,15 @@ struct Sched {
     if (cta >= G) waves = 0;
     started = false;
   }
-  // First tile of share c, and the share that holds tile x (without waves, shares differ by at
-  // most one tile).
-  __device__ __forceinline__ long long share(int c) const {
+  // Start of share c, and the share that holds place x of the line (without waves, shares
+  // differ by at most one tile).
+  __device__ __forceinline__ int share(int c) const {
     return balanced ? mem->bounds[c] : base + quot * c + min(c, rem);
   }
-  __device__ __forceinline__ int share_of(long long x) const {
+  __device__ __forceinline__ int share_of(int x) const {
     if (balanced) return last_upto(mem->bounds, G, x);
-    const long long y = x - base, big = (quot + 1) * rem;
-    return (int)(y < big ? y / (quot + 1) : rem + (y - big) / quot);
+    const int y = x - base, big = (quot + 1) * rem;
+    return y < big ? y / (quot + 1) : rem + (y - big) / quot;
   }
 
   __device__ __forceinline__ int wave_unit(int w, int c) const { return w * G + (w & 1 ? G - 1 - c : c); }
@@ -274,16 +276,16 @@ struct Sched {
     const int left = u - mem->units[n], nb = blocks(r);
     h = left / nb;
     blk = left - h * nb;
-    unit0 = mem->pre[n] + (mem->pre[n + 1] - mem->pre[n]) / s.Hkv * h + cost_before(blk);
+    unit0 = mem->pre[n] + s.by_hkv.div(mem->pre[n + 1] - mem->pre[n]) * h + cost_before(blk);
   }
 
   // Request, head, row block and start of the unit that holds tile `x`; whole warps.
-  __device__ void locate(long long x) {
+  __device__ void locate(int x) {
     n = last_upto(mem->pre, s.nn, x);
     r = load_req(s, n);
-    const long long per = (mem->pre[n + 1] - mem->pre[n]) / s.Hkv;
-    long long left = x - mem->pre[n];
-    h = (int)(left / per);
+    const int per = s.by_hkv.div(mem->pre[n + 1] - mem->pre[n]);
+    int left = x - mem->pre[n];
+    h = min(left / per, s.Hkv - 1);
     left -= per * h;
     // 32 row blocks at a time: the first whose inclusive sum passes what is left
     const int nb = blocks(r), lane = threadIdx.x & 31;
@@ -325,19 +327,13 @@ struct Sched {
       it->slot = 0;
       return true;
     }
-    if (!started) {  // boundaries within a unit's own cost come before it
-      if (pos < total) {
-        if (end < total) {
-          locate(end);
-          if (end <= unit0 + s.unit_cost) end = unit0;
-        }
-        locate(pos);
-        if (pos <= unit0 + s.unit_cost) pos = first = unit0;
-      }
+    if (pos >= end) return false;
+    if (!started) {
+      locate(pos);
       started = true;
-      if (pos >= end) return false;
+      // boundaries within a unit's own cost come before it: the share's start here, its end below
+      if (pos <= unit0 + s.unit_cost) pos = first = unit0;
     } else {
-      if (pos >= end) return false;
       if (++blk == blocks(r)) {
         blk = 0;
         if (++h == s.Hkv) {
@@ -349,16 +345,20 @@ struct Sched {
       }
       unit0 = pos;
     }
+    if (end <= unit0 + s.unit_cost) {
+      pos = end;
+      return false;
+    }
     int lo;
     bool empty;
     const int c = tiles(r, blk, &lo, &empty) + s.unit_cost;
-    const long long stop = min(unit0 + c, end);
+    const int stop = min(unit0 + c, end);
     it->n = n;
     it->h = h;
     it->blk = blk;
     it->r = r;
-    it->tb = empty || pos == unit0 ? lo : lo + (int)(pos - unit0) - s.unit_cost;
-    it->te = empty ? 0 : lo + (int)(stop - unit0) - s.unit_cost;
+    it->tb = empty || pos == unit0 ? lo : lo + (pos - unit0) - s.unit_cost;
+    it->te = empty ? 0 : lo + (stop - unit0) - s.unit_cost;
     it->whole = pos == unit0 && stop == unit0 + c;
     it->slot = 2 * cta + (unit0 > first ? 1 : 0);
     pos = stop;

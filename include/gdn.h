@@ -508,8 +508,10 @@ int gdn_paged_write(const void* k, const void* v, const int32_t* slot_map, void*
  *            every request, not for rows outside all of them
  * workspace  device scratch of gdn_paged_attention_workspace_bytes(...) bytes, no
  *            initialisation needed; calls that overlap on the GPU need one each
- * max_q_len  the most new tokens of a request (a larger value costs speed only)
- * max_seq_len the most tokens of a sequence, 0 if not known (for speed only)
+ * max_q_len  the most new tokens of a request: chooses the kernels, so that a larger value
+ *            costs speed only
+ * max_seq_len the most tokens of a sequence, 0 if not known (then the tables' room): a bound
+ *            on the work of one request, which has to stay below 2^31 tiles
  * scale      positive
  *
  * Scores, softmax and sums are fp32; out is rounded once.  Deterministic.  Asynchronous;
