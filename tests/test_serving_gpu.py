@@ -507,3 +507,23 @@ def test_attention_caches_beyond_l2():
             ref = R.attention(q[cu[n] + i, h][None, None], kk, vv, p, d ** -0.5, 0)
             got = (out[cu[n] + i, h].double().cpu()[None, None], lse[cu[n] + i, h].double().cpu()[None, None], ref)
             _check_attend([got], d, [kv[n]], True, f"token {i} head {h}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_step_bad_tokens_reach_later_ones_only(dtype):
+    """A non-finite value of one token leaves the tokens before it, the other rows and the other
+    requests as they are."""
+    q, k, v, la, beta, pool, index, _ = _step_inputs([7, 3], 2, 2, 64, 64, dtype, 11)
+    run = lambda v, k: gdn.recurrent_step(  # noqa: E731
+        *(x.to(DEV) for x in (q, k, v, la, beta)), pool.to(DEV), index.to(DEV), _i32([0, 7, 10]))
+    good = run(v, k)
+    v2, k2 = v.clone(), k.clone()
+    v2[4, 0, 5] = math.inf
+    bad = run(v2, k2)
+    assert not torch.isfinite(bad[4:7, 0, 5]).any()
+    bad[4:7, 0, 5] = good[4:7, 0, 5]
+    assert torch.equal(bad, good)
+    k2[5, 1] = math.nan
+    bad = run(v, k2)
+    assert torch.equal(bad[:5], good[:5]) and torch.equal(bad[7:], good[7:]) and torch.equal(bad[:, 0], good[:, 0])
+    assert torch.isnan(bad[5:7, 1]).all()
