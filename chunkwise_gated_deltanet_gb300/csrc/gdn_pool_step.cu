@@ -7,12 +7,31 @@
 // (Nyysyyan, "Gated-DeltaNet" section, first equation block), with key head
 // h / (H / Hk).  The state is read once and written once however many tokens there are.
 //
-// For a few tokens this is bound by HBM (8 dk dv bytes a (request, head)).  Token by token on
-// the CUDA cores the arithmetic passes that at a few tokens: 96 packed multiply-adds and as
-// much again for reductions and operands, a warp, 16 rows and token (1 to 8 tokens x 256
-// requests of 16 heads took 122 us, up to 64 tokens x 48 requests of 32 heads 183 us).  So
-// tokens go kC = 8 at a time, in the chunk form with S0 the state before them, D_ts the product
-// of alpha_{s+1} .. alpha_t and gamma_t that of alpha_0 .. alpha_t:
+// Bound by HBM for a few tokens (8 dk dv bytes a (request, head)), by arithmetic from about a
+// dozen on (8 dk dv operations a token).  Two kernels, chosen by the tokens a request has on
+// average, T / N (measured at 16 and 32 heads of 128, bf16; 1 to 8 tokens x 256 requests, 1 to
+// 64 tokens x 48 requests):
+//
+//   up to 8   token by token on the CUDA cores           TOKENS us         183 us
+//   above     8 tokens at a time on the tensor cores     141 us            152 us
+//
+// Both stage k, q, v of 8 tokens by cp.async while the 8 before are computed, and read and
+// write a unit's state, one (request, head), once.
+//
+// Token by token.  S is held as A S~ with A the product of the alphas since the tokens were
+// staged, which leaves one multiply-add an element for the update:
+//     u = beta (v - A p~),  S~ <- S~ + (u / A) k^T,  o = A s~ + u (k . q),
+// p~ = S~ k, s~ = S~ q.  The last A is multiplied in after the 8 tokens; where A would fall
+// below 2^-60 (strong decay, alpha = 0), S is scaled token by token.  Products are packed pairs
+// (fma.rn.f32x2).  A lane holds 4 rows of S, an eighth of the columns each, so that a read of k
+// or q serves 4 rows; the 8 sums of a row quartet are reduced over the 8 lanes together.  Of
+// such short units most of the time would be their start: indices, then state and tokens, each
+// an HBM latency.  So a CTA takes further units over from CTAs that have not started (cluster
+// launch control), two ahead: it looks up the indices of the one while the state and tokens of
+// the other come into shared memory and a third is computed.
+//
+// 8 tokens at a time, the chunk form: with S0 the state before them, D_ts the product of
+// alpha_{s+1} .. alpha_t and gamma_t that of alpha_0 .. alpha_t:
 //
 //     u_t = beta_t (v_t - gamma_t S0 k_t) - sum_{s<t} beta_t D_ts (k_t . k_s) u_s
 //     o_t = gamma_t S0 q_t + sum_{s<=t} D_ts (q_t . k_s) u_s
@@ -23,19 +42,19 @@
 // s < t are eight steps in registers.  A warp has 16 rows of S in the accumulators' layout for
 // the whole call.  The same registers are the products' left operand: an accumulator's columns
 // 2 t and 2 t + 1 stand for the operand's t and t + 4, and the right operands are laid out in
-// shared memory in that order, a 16-byte piece a lane (hi and lo of both values).  The next
-// tokens' k, q, v come by cp.async under this chunk's products.
+// shared memory in that order, a 16-byte piece a lane (hi and lo of both values).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <type_traits>
 
 #include "gdn_internal.h"
+#include "tc_common.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kC = 8;  // tokens at a time
+constexpr int kTok = 8;  // tokens staged at a time
 
 template <bool BF16>
 __device__ __forceinline__ void st1f(void* p, size_t i, float x) {
@@ -43,6 +62,17 @@ __device__ __forceinline__ void st1f(void* p, size_t i, float x) {
     reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
   else
     reinterpret_cast<float*>(p)[i] = x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void st4f(void* p, size_t i, float4 x) {
+  if (BF16) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p) + i) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = x;
+  }
 }
 
 // x = hi + lo with hi of TF32's 11 significant bits; lo is cut to them by the product.
@@ -80,25 +110,404 @@ __device__ __forceinline__ void copy4(void* to, const void* from, bool there) {
                : "memory");
 }
 
+// The coming 8 tokens as they are, zeros past the request's.
 template <int DK, bool BF16>
-struct StepSmem {
+struct StepRaw {
   static constexpr int kSize = BF16 ? 2 : 4, kPad = 16 / kSize;  // rows padded: other banks
   using El = typename std::conditional<BF16, __nv_bfloat16, float>::type;
-  // the coming chunk's tokens as they are, zeros past the request's
-  alignas(16) El k[kC][DK + kPad];
-  alignas(16) El q[kC][DK + kPad];
-  alignas(16) El v[kC][128 + kPad];
-  alignas(16) float raw_la[kC];
-  alignas(16) float raw_beta[kC];
+  alignas(16) El k[kTok][DK + kPad];
+  alignas(16) El q[kTok][DK + kPad];
+  alignas(16) El v[kTok][128 + kPad];
+  alignas(16) float la[kTok];
+  alignas(16) float beta[kTok];
+};
+
+// Asks for a CTA of this grid that has not started; the answer arrives at `bar` (16 bytes).
+__device__ __forceinline__ void take_cta(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// Its index in x, or -1 if there was none left.
+__device__ __forceinline__ int taken_cta(const uint4* answer) {
+  uint32_t ok, x = 0;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
+// One (request, head).
+struct StepUnit {
+  int n, h, t0, t1, slot;  // slot < 0: no state
+  bool fresh;
+  __device__ __forceinline__ StepUnit(const StepArgs& a, int unit, int cu0, int cu1, int at, int context) {
+    n = unit / a.H;
+    h = unit - n * a.H;
+    t0 = min(max(cu0, 0), a.T);
+    t1 = min(max(cu1, t0), a.T);
+    slot = at < a.slots ? at : -1;
+    fresh = a.context_lens != nullptr && context <= 0;
+  }
+};
+__device__ __forceinline__ StepUnit first_unit(const StepArgs& a) {
+  const int n = blockIdx.x / a.H;
+  return StepUnit(a, blockIdx.x, __ldg(a.cu_seqlens + n), __ldg(a.cu_seqlens + n + 1), __ldg(a.state_index + n),
+                  a.context_lens ? __ldg(a.context_lens + n) : 1);
+}
+
+// The 8 tokens from tb on of unit w, by the whole CTA.
+template <int DK, bool BF16>
+__device__ __forceinline__ void stage(StepRaw<DK, BF16>& raw, const StepArgs& a, const StepUnit& w, int tb) {
+  using El = typename StepRaw<DK, BF16>::El;
+  constexpr int V = 16 / StepRaw<DK, BF16>::kSize;
+  const int tid = threadIdx.x, nthreads = blockDim.x, dv = a.dv, hk = w.h / (a.H / a.Hk);
+  const El* k = reinterpret_cast<const El*>(a.k) + hk * DK;
+  const El* q = reinterpret_cast<const El*>(a.q) + hk * DK;
+  const El* v = reinterpret_cast<const El*>(a.v) + (size_t)w.h * dv;
+  for (int e = tid; e < kTok * (DK / V); e += nthreads) {
+    const int j = e / (DK / V), c = (e % (DK / V)) * V;
+    const bool in = tb + j < w.t1;
+    const size_t at = in ? tb + j : tb;
+    copy16(&raw.k[j][c], k + at * a.k_stride + c, in);
+    copy16(&raw.q[j][c], q + at * a.q_stride + c, in);
+  }
+  for (int e = tid; e < kTok * (dv / V); e += nthreads) {
+    const int j = e / (dv / V), c = (e % (dv / V)) * V;
+    const bool in = tb + j < w.t1;
+    copy16(&raw.v[j][c], v + (size_t)(in ? tb + j : tb) * a.v_stride + c, in);
+  }
+  if (tid < 2 * kTok) {
+    const int j = tid & 7;
+    const bool in = tb + j < w.t1;
+    const size_t at = (size_t)(in ? tb + j : tb) * a.H + w.h;
+    if (tid < kTok)
+      copy4(&raw.la[j], a.log_alpha + at, in);
+    else
+      copy4(&raw.beta[j], a.beta + at, in);
+  }
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void landed() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ uint64_t both(float a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
+  return r;
+}
+__device__ __forceinline__ float sum_of(uint64_t x) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+  return a + b;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <int DK, bool BF16>
+struct TokenSmem {
+  StepRaw<DK, BF16> raw;
+  alignas(16) float k[kTok][DK];
+  alignas(16) float q[kTok][DK];
+  alignas(16) float v[kTok][128];
+  alignas(16) float o[kTok][128];
+  alignas(16) float4 gate[kTok];  // A, beta, 1 / A, k . q
+  float alpha[kTok], A[kTok];
+  int slow;
+  // the answer of the launch control, and of every second unit its number (-1: none) and
+  // indices (cu_seqlens[n], cu_seqlens[n + 1], state_index[n], context_lens[n])
+  alignas(16) uint4 taken;
+  uint64_t s_full, taken_full;
+  int id[2], idx[2][4], abort_flag;
+};
+
+template <int DK>
+constexpr int kTokenRows = 32 / (DK >= 32 ? 8 : 4) * 4;  // rows a warp
+
+template <int DK, bool BF16>
+__global__ void __launch_bounds__(256, 2) step_tokens_kernel(const __grid_constant__ StepArgs a, int* status) {
+  constexpr int L = DK >= 32 ? 8 : 4, R = 4;  // lanes a row, rows a lane
+  constexpr int NP = DK / L / 2;              // pairs of S a lane and row
+  __shared__ TokenSmem<DK, BF16> sm;
+  extern __shared__ __align__(16) float state[];  // the coming unit's state
+  using El = typename StepRaw<DK, BF16>::El;
+
+  const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int dv = a.dv, dv4 = dv / 4;
+  // lane `sub` of a row group: columns 4 (sub + L i) .. + 3; rows row .. row + 3
+  const int sub = lane % L;
+  const int row = (warp * (32 / L) + lane / L) * R;
+  const bool live = row < dv;
+  auto place = [&](const StepUnit& w) { return a.pool + ((size_t)w.slot * a.H + w.h) * dv * DK; };
+  // a unit's state on its way into shared memory, and its first tokens
+  auto begin = [&](const StepUnit& w) {
+    if (w.t1 > w.t0 && w.slot >= 0) stage(sm.raw, a, w, w.t0);
+    if (tid == 0) {
+      if (w.t1 > w.t0 && w.slot >= 0 && !w.fresh) {
+        mbar_arrive_expect_tx(&sm.s_full, (uint32_t)(dv * DK * 4));
+        bulk_load(state, place(w), (uint32_t)(dv * DK * 4), &sm.s_full);
+      } else {
+        mbar_arrive(&sm.s_full);
+      }
+    }
+  };
+  // thread 0: the answer to the i-th request, as unit i + 1; its indices on their way
+  auto look_up = [&](uint32_t i) {
+    int id = -1;
+    if (wait_bar(&sm.taken_full, i & 1, &sm.abort_flag, false)) id = taken_cta(&sm.taken);
+    sm.id[(i + 1) & 1] = id;
+    if (id < 0) return;
+    fence_async_smem();  // read before the next answer is written
+    take_cta(&sm.taken, &sm.taken_full);
+    const int n = id / a.H;
+    int* to = sm.idx[(i + 1) & 1];
+    copy4(to, a.cu_seqlens + n, true);
+    copy4(to + 1, a.cu_seqlens + n + 1, true);
+    copy4(to + 2, a.state_index + n, true);
+    copy4(to + 3, a.context_lens ? a.context_lens + n : a.state_index + n, true);
+  };
+
+  if (tid == 0) {
+    sm.abort_flag = 0;
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.taken_full, 1);
+    fence_mbarrier_init();
+    take_cta(&sm.taken, &sm.taken_full);
+  }
+  __syncthreads();
+  StepUnit now = first_unit(a);
+  begin(now);
+  if (tid == 0) look_up(0);
+  commit();
+
+  for (uint32_t unit = 0;; ++unit) {
+    const int h = now.h, t0 = now.t0, t1 = now.t1;
+    const bool work = t1 > t0 && now.slot >= 0;
+    int more = -1;
+    StepUnit next = now;
+    auto advance = [&] {  // the next unit, whose indices have landed: its state and tokens set out
+      more = sm.id[(unit + 1) & 1];
+      if (more < 0) return;
+      const int* x = sm.idx[(unit + 1) & 1];
+      next = StepUnit(a, more, x[0], x[1], x[2], x[3]);
+      begin(next);
+      if (tid == 0) look_up(unit + 1);
+      commit();
+    };
+    wait_bar(&sm.s_full, unit & 1, &sm.abort_flag, false);
+    uint64_t s[R][NP];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < NP; i += 2) {
+        ulonglong2 x = make_ulonglong2(0, 0);
+        if (live && work && !now.fresh)
+          x = *reinterpret_cast<const ulonglong2*>(state + (row + r) * DK + 4 * sub + 2 * L * i);
+        s[r][i] = x.x;
+        s[r][i + 1] = x.y;
+      }
+    fence_async_smem();  // read before the next state is copied over it
+    if (!work) {
+      landed();
+      __syncthreads();
+      advance();
+      // no tokens: the state stays as it is; no state: the outputs are zeros
+      for (int e = tid; e < (t1 - t0) * dv; e += nthreads)
+        st1f<BF16>(a.out, ((size_t)(t0 + e / dv) * a.H + h) * dv + e % dv, 0.f);
+    }
+    for (int tb = t0; work && tb < t1; tb += kTok) {
+      const int nt = min(kTok, t1 - tb);
+      landed();
+      __syncthreads();
+      auto wide = [](const El* p) {  // four elements as fp32
+        if (BF16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                             __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+        }
+        return *reinterpret_cast<const float4*>(p);
+      };
+      for (int e = tid; e < nt * (DK / 4); e += nthreads) {
+        const int j = e / (DK / 4), c = (e % (DK / 4)) * 4;
+        *reinterpret_cast<float4*>(&sm.k[j][c]) = wide(&sm.raw.k[j][c]);
+        *reinterpret_cast<float4*>(&sm.q[j][c]) = wide(&sm.raw.q[j][c]);
+      }
+      for (int e = tid; e < nt * dv4; e += nthreads) {
+        const int j = e / dv4, c = (e - j * dv4) * 4;
+        *reinterpret_cast<float4*>(&sm.v[j][c]) = wide(&sm.raw.v[j][c]);
+      }
+      // k . q of each token, a warp a token, and in the first lanes of its warp the gates
+      for (int j = warp; j < nt; j += nthreads >> 5) {
+        float x = 0.f;
+        for (int c = 4 * lane; c < DK; c += 128) {
+          const float4 kk = wide(&sm.raw.k[j][c]), qq = wide(&sm.raw.q[j][c]);
+          x = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, x))));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        // products of the alphas up to each staged token
+        const float al = lane < nt ? expf(sm.raw.la[lane]) : 1.f;
+        float A = al;
+#pragma unroll
+        for (int o = 1; o < kTok; o <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, A, o);
+          if (lane >= o) A *= y;
+        }
+        const bool slow = __any_sync(0xffffffffu, lane < nt && !(A >= 0x1p-60f));
+        const float Aj = slow ? 1.f : __shfl_sync(0xffffffffu, A, j);
+        const float alj = __shfl_sync(0xffffffffu, al, j);
+        if (lane == 0) {
+          sm.gate[j] = make_float4(Aj, sm.raw.beta[j], 1.f / Aj, x);
+          sm.alpha[j] = alj;
+          sm.slow = slow;  // the same from every warp
+        }
+      }
+      __syncthreads();
+      if (tb + kTok < t1) {
+        stage(sm.raw, a, now, tb + kTok);
+        commit();
+      } else {
+        advance();
+      }
+      const bool slow = sm.slow != 0;
+      for (int j = 0; j < nt; ++j) {
+        const float4 gate = sm.gate[j];
+        const float A = gate.x;
+        if (slow) {
+          const uint64_t al = both(sm.alpha[j]);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) s[r][i] = mul2(s[r][i], al);
+        }
+        uint64_t kk[NP];
+        float x[2 * R];  // p~ of the rows, then s~
+        {
+          uint64_t p[R], q[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) p[r] = q[r] = 0;
+#pragma unroll
+          for (int i = 0; i < NP; i += 2) {
+            const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&sm.k[j][4 * sub + 2 * L * i]);
+            const ulonglong2 q2 = *reinterpret_cast<const ulonglong2*>(&sm.q[j][4 * sub + 2 * L * i]);
+            kk[i] = k2.x;
+            kk[i + 1] = k2.y;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              p[r] = fma2(s[r][i], k2.x, p[r]);
+              q[r] = fma2(s[r][i], q2.x, q[r]);
+              p[r] = fma2(s[r][i + 1], k2.y, p[r]);
+              q[r] = fma2(s[r][i + 1], q2.y, q[r]);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            x[r] = sum_of(p[r]);
+            x[R + r] = sum_of(q[r]);
+          }
+        }
+        float w[R];  // u / A of the four rows
+        if (L == 8) {
+          // lane `sub` ends with the total of x[sub]: halves exchanged with lanes 4, 2, 1 apart
+          float y4[4], y2[2], y;
+          const bool b4 = sub & 4, b2 = sub & 2, b1 = sub & 1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y4[i] = (b4 ? x[4 + i] : x[i]) + __shfl_xor_sync(0xffffffffu, b4 ? x[i] : x[4 + i], 4);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            y2[i] = (b2 ? y4[2 + i] : y4[i]) + __shfl_xor_sync(0xffffffffu, b2 ? y4[i] : y4[2 + i], 2);
+          y = (b1 ? y2[1] : y2[0]) + __shfl_xor_sync(0xffffffffu, b1 ? y2[0] : y2[1], 1);
+          // lanes 0-3: u of row `sub`; lanes 4-7: the output of row `sub` - 4
+          const float u = gate.y * fmaf(-A, y, live ? sm.v[j][row + (sub & 3)] : 0.f);
+          const float ur = __shfl_sync(0xffffffffu, u, (lane & ~7) + (sub & 3));
+          if (live && sub >= 4) sm.o[j][row + sub - 4] = fmaf(A, y, ur * gate.w);
+          const float wr = ur * gate.z;
+#pragma unroll
+          for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, wr, (lane & ~7) + r);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2 * R; ++i)
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float u = gate.y * fmaf(-A, x[r], live ? sm.v[j][row + r] : 0.f);
+            if (live && sub == 0) sm.o[j][row + r] = fmaf(A, x[R + r], u * gate.w);
+            w[r] = u * gate.z;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint64_t w2 = both(w[r]);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) s[r][i] = fma2(w2, kk[i], s[r][i]);
+        }
+      }
+      if (!slow) {
+        const uint64_t A = both(sm.gate[nt - 1].x);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < NP; ++i) s[r][i] = mul2(s[r][i], A);
+      }
+      // a warp's own rows: no other warp has a part in them
+      __syncwarp();
+      constexpr int W4 = kTokenRows<DK> / 4;
+      for (int e = lane; e < nt * W4; e += 32) {
+        const int j = e / W4, c = warp * kTokenRows<DK> + (e % W4) * 4;
+        if (c < dv)
+          st4f<BF16>(a.out, ((size_t)(tb + j) * a.H + h) * dv + c, *reinterpret_cast<const float4*>(&sm.o[j][c]));
+      }
+    }
+    if (work && live) {
+      float* S = place(now) + (size_t)row * DK + 4 * sub;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < NP; i += 2)
+          *reinterpret_cast<ulonglong2*>(S + (size_t)r * DK + 2 * L * i) = make_ulonglong2(s[r][i], s[r][i + 1]);
+    }
+    if (more < 0) break;
+    now = next;
+  }
+  if (sm.abort_flag && tid == 0) {  // let a copy still in flight land before the CTA ends
+    const uint64_t tw = globaltimer_ns();
+    while (globaltimer_ns() - tw < 50000ull) {
+    }
+    atomicOr(status, sm.abort_flag);
+  }
+}
+
+template <int DK, bool BF16>
+struct ChunkSmem {
+  StepRaw<DK, BF16> raw;
   // right operands, a piece a lane (g = lane / 4, t = lane % 4) and 8 columns: k and q of token
   // g at the columns of the lane's accumulators, and k of tokens 2 t, 2 t + 1 at column g's
   alignas(16) uint4 kd[DK / 8][32], qd[DK / 8][32], ku[DK / 8][32];
   // of tokens 2 t, 2 t + 1 and s: beta_t D_ts k_t . k_s (s < t, else 0) of both, D_ts q_t . k_s
   // (s <= t) of both
-  alignas(16) float4 m[kC][4];
-  float decay[kC][kC];       // D_ts
-  float part[8][16][kC + 1]; // a warp's part of k_i . k_j (rows 0-7) and q_i . k_j (8-15)
-  float beta[kC], gamma[kC], last[kC];
+  alignas(16) float4 m[kTok][4];
+  float decay[kTok][kTok];      // D_ts
+  float part[8][16][kTok + 1];  // a warp's part of k_i . k_j (rows 0-7) and q_i . k_j (8-15)
+  float beta[kTok], gamma[kTok], last[kTok];
 };
 // Column of an accumulator's entry: tile n of 8, column j of the tile.  A lane's entries of
 // tiles 2 m and 2 m + 1 are the four consecutive columns 16 m + 4 t ..
@@ -107,101 +516,73 @@ __device__ __forceinline__ int col_of(int n, int j) {
 }
 
 template <int DK, bool BF16>
-__global__ void __launch_bounds__(256, 2) pool_step_kernel(const __grid_constant__ StepArgs a) {
+__global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_constant__ StepArgs a) {
   constexpr int NT = DK / 8;  // column tiles of S
-  __shared__ StepSmem<DK, BF16> sm;
+  __shared__ ChunkSmem<DK, BF16> sm;
+  using El = typename StepRaw<DK, BF16>::El;
 
-  const int n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, hk = h / (a.H / a.Hk);
-  const int t0 = min(max(__ldg(a.cu_seqlens + n), 0), a.T);
-  const int t1 = min(max(__ldg(a.cu_seqlens + n + 1), t0), a.T);
+  const StepUnit now = first_unit(a);
+  const int h = now.h, t0 = now.t0, t1 = now.t1;
   if (t0 == t1) return;  // no tokens: the state stays as it is
-  const int slot = __ldg(a.state_index + n);
   const int tid = threadIdx.x, nthreads = blockDim.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = tid >> 5, nwarps = nthreads >> 5;
   const int dv = a.dv, row = warp * 16 + g;  // this lane's rows: row and row + 8
-  if (slot < 0 || slot >= a.slots) {               // no state: the outputs are zeros
+  if (now.slot < 0) {                        // no state: the outputs are zeros
     for (int e = tid; e < (t1 - t0) * dv; e += nthreads)
       st1f<BF16>(a.out, ((size_t)(t0 + e / dv) * a.H + h) * dv + e % dv, 0.f);
     return;
   }
-  const bool fresh = a.context_lens != nullptr && __ldg(a.context_lens + n) <= 0;
-  using Sm = StepSmem<DK, BF16>;
-  using El = typename Sm::El;
-  auto stage = [&](int tb) {  // the chunk from token tb on
-    constexpr int V = 16 / Sm::kSize;
-    const El* k = reinterpret_cast<const El*>(a.k) + hk * DK;
-    const El* q = reinterpret_cast<const El*>(a.q) + hk * DK;
-    const El* v = reinterpret_cast<const El*>(a.v) + (size_t)h * dv;
-    for (int e = tid; e < kC * (DK / V); e += nthreads) {
-      const int j = e / (DK / V), c = (e % (DK / V)) * V;
-      const bool in = tb + j < t1;
-      const size_t at = in ? tb + j : tb;
-      copy16(&sm.k[j][c], k + at * a.k_stride + c, in);
-      copy16(&sm.q[j][c], q + at * a.q_stride + c, in);
-    }
-    for (int e = tid; e < kC * (dv / V); e += nthreads) {
-      const int j = e / (dv / V), c = (e % (dv / V)) * V;
-      const bool in = tb + j < t1;
-      copy16(&sm.v[j][c], v + (size_t)(in ? tb + j : tb) * a.v_stride + c, in);
-    }
-    if (tid < 2 * kC) {
-      const int j = tid & 7;
-      const bool in = tb + j < t1;
-      const size_t at = (size_t)(in ? tb + j : tb) * a.H + h;
-      if (tid < kC)
-        copy4(&sm.raw_la[j], a.log_alpha + at, in);
-      else
-        copy4(&sm.raw_beta[j], a.beta + at, in);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  stage(t0);
-  float* S = a.pool + (((size_t)slot * a.H + h) * dv + row) * DK + 4 * t;
+  stage(sm.raw, a, now, t0);
+  commit();
+  float* S = a.pool + (((size_t)now.slot * a.H + h) * dv + row) * DK + 4 * t;
   float s[NT][4];
 #pragma unroll
   for (int m = 0; m < NT; m += 2)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!fresh) x = *reinterpret_cast<const float4*>(S + (size_t)(8 * r) * DK + 8 * m);
+      if (!now.fresh) x = *reinterpret_cast<const float4*>(S + (size_t)(8 * r) * DK + 8 * m);
       s[m][2 * r] = x.x;
       s[m][2 * r + 1] = x.y;
       s[m + 1][2 * r] = x.z;
       s[m + 1][2 * r + 1] = x.w;
     }
 
-  for (int tb = t0; tb < t1; tb += kC) {
-    const int nt = min(kC, t1 - tb);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  for (int tb = t0; tb < t1; tb += kTok) {
+    const int nt = min(kTok, t1 - tb);
+    landed();
     __syncthreads();
     // from the staged tokens: the operands, the gates, and v of this lane's rows
     auto f = [](El x) { return (float)x; };
     for (int e = tid; e < NT * 32; e += nthreads) {
       const int m = e >> 5, lg = (e & 31) >> 2, lt = e & 3, c = col_of(m, 2 * lt), cg = col_of(m, lg);
-      sm.kd[m][e & 31] = tf_pair(f(sm.k[lg][c]), f(sm.k[lg][c + 1]));
-      sm.qd[m][e & 31] = tf_pair(f(sm.q[lg][c]), f(sm.q[lg][c + 1]));
-      sm.ku[m][e & 31] = tf_pair(f(sm.k[2 * lt][cg]), f(sm.k[2 * lt + 1][cg]));
+      sm.kd[m][e & 31] = tf_pair(f(sm.raw.k[lg][c]), f(sm.raw.k[lg][c + 1]));
+      sm.qd[m][e & 31] = tf_pair(f(sm.raw.q[lg][c]), f(sm.raw.q[lg][c + 1]));
+      sm.ku[m][e & 31] = tf_pair(f(sm.raw.k[2 * lt][cg]), f(sm.raw.k[2 * lt + 1][cg]));
     }
-    for (int e = tid; e < kC * kC; e += nthreads) {
+    for (int e = tid; e < kTok * kTok; e += nthreads) {
       const int i = e >> 3, j = e & 7;  // D_ij, and in the row's end gamma_j and D_7j
       float x = 0.f;
-      for (int u = j + 1; u <= i; ++u) x += sm.raw_la[u];
+      for (int u = j + 1; u <= i; ++u) x += sm.raw.la[u];
       sm.decay[i][j] = j > i ? 0.f : expf(x);
-      if (i == kC - 1) {
+      if (i == kTok - 1) {
         sm.last[j] = expf(x);
         float y = 0.f;
-        for (int u = 0; u <= j; ++u) y += sm.raw_la[u];
+        for (int u = 0; u <= j; ++u) y += sm.raw.la[u];
         sm.gamma[j] = expf(y);
-        sm.beta[j] = sm.raw_beta[j];
+        sm.beta[j] = sm.raw.beta[j];
       }
     }
     float v[2][2];  // tokens 2 t, 2 t + 1 (second index)
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) v[r][b] = f(sm.v[2 * t + b][row + 8 * r]);
+      for (int b = 0; b < 2; ++b) v[r][b] = f(sm.raw.v[2 * t + b][row + 8 * r]);
     __syncthreads();
-    if (tb + kC < t1) stage(tb + kC);
+    if (tb + kTok < t1) {
+      stage(sm.raw, a, now, tb + kTok);
+      commit();
+    }
     // the tokens' products with each other: a warp takes every (warps)-th tile of columns
     {
       float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -214,14 +595,14 @@ __global__ void __launch_bounds__(256, 2) pool_step_kernel(const __grid_constant
       for (int e = 0; e < 4; ++e) sm.part[warp][g + 8 * (e >> 1)][2 * t + (e & 1)] = c[e];
     }
     __syncthreads();
-    for (int e = tid; e < 2 * kC * kC; e += nthreads) {
+    for (int e = tid; e < 2 * kTok * kTok; e += nthreads) {
       const int i = e >> 3, j = e & 7;  // row i of part, token j
       const int ti = i & 7;
       float dot = 0.f;
       for (int w = 0; w < min(nwarps, NT); ++w) dot += sm.part[w][i][j];
       float* to = reinterpret_cast<float*>(&sm.m[j][ti >> 1]) + (ti & 1);
       const float x = j > ti ? 0.f : sm.decay[ti][j] * dot;
-      if (i >= kC)
+      if (i >= kTok)
         to[2] = x;
       else
         to[0] = j < ti ? sm.beta[ti] * x : 0.f;
@@ -256,7 +637,7 @@ __global__ void __launch_bounds__(256, 2) pool_step_kernel(const __grid_constant
       }
     }
 #pragma unroll
-    for (int j = 0; j < kC; ++j) {
+    for (int j = 0; j < kTok; ++j) {
       const float4 m = sm.m[j][t];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -286,7 +667,7 @@ __global__ void __launch_bounds__(256, 2) pool_step_kernel(const __grid_constant
         lo[2 * b + r] = tf_lo(x, hi[2 * b + r]);
       }
     }
-    const float gamma = sm.gamma[kC - 1];
+    const float gamma = sm.gamma[kTok - 1];
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
 #pragma unroll
@@ -302,16 +683,26 @@ __global__ void __launch_bounds__(256, 2) pool_step_kernel(const __grid_constant
           make_float4(s[m][2 * r], s[m][2 * r + 1], s[m + 1][2 * r], s[m + 1][2 * r + 1]);
 }
 
-template <int DK>
-cudaError_t launch_dk(const StepArgs& a, cudaStream_t stream) {
+template <int DK, bool BF16>
+cudaError_t launch_step(const StepArgs& a, cudaStream_t stream) {
   const long long ctas = (long long)a.N * a.H;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int threads = 32 * (a.dv / 16);
-  if (a.bf16)
-    pool_step_kernel<DK, true><<<(unsigned)ctas, threads, 0, stream>>>(a);
-  else
-    pool_step_kernel<DK, false><<<(unsigned)ctas, threads, 0, stream>>>(a);
+  if ((long long)a.T > (long long)kTok * a.N) {
+    step_chunks_kernel<DK, BF16><<<(unsigned)ctas, 32 * (a.dv / 16), 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  int* status = nullptr;
+  cudaError_t e = tc_status_address(&status);
+  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> done{0};
+  if ((e = ensure_smem_cap(step_tokens_kernel<DK, BF16>, DK * 128 * 4, done, true)) != cudaSuccess) return e;
+  const int threads = 32 * ((a.dv + kTokenRows<DK> - 1) / kTokenRows<DK>);
+  step_tokens_kernel<DK, BF16><<<(unsigned)ctas, threads, DK * a.dv * 4, stream>>>(a, status);
   return cudaGetLastError();
+}
+template <int DK>
+cudaError_t launch_dk(const StepArgs& a, cudaStream_t stream) {
+  return a.bf16 ? launch_step<DK, true>(a, stream) : launch_step<DK, false>(a, stream);
 }
 
 }  // namespace
