@@ -17,14 +17,41 @@
 namespace gdn {
 namespace {
 
+// Bound by the CUDA cores' multiply-adds where there are many rows (packed pairs,
+// fma.rn.f32x2), by latency where there are few; fp32 tiles come by cp.async, one ahead.
 constexpr int kThreads = 256;
 constexpr int kBN = 64, kSimtRequests = 1024;
 template <int M>
 using SimtSched = Sched<M, kBN, kSimtRequests, false>;
 
-template <int D, int M>
+// K and V tiles: two of each where they come by cp.async.
+template <int D, bool BF16>
+constexpr int kTiles = BF16 ? 1 : 2;
+template <int D, int M, bool BF16>
 constexpr int simt_smem() {
-  return (M * D + kBN * (D + 4) + kBN * D + M * (kBN + 4)) * 4 + (int)sizeof(typename SimtSched<M>::Mem);
+  return (M * D + kTiles<D, BF16> * (kBN * (D + 4) + kBN * D) + M * (kBN + 4)) * 4 +
+         (int)sizeof(typename SimtSched<M>::Mem);
+}
+
+__device__ __forceinline__ void copy16(void* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // Four consecutive elements as fp32.
@@ -49,8 +76,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
   extern __shared__ __align__(16) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem);  // [M][D], scaled to log2 units
   float* ks = qs + M * D;                      // [64][D + 4]
-  float* vs = ks + kBN * (D + 4);              // [64][D]
-  float* ps = vs + kBN * D;                    // [M][64 + 4]
+  float* vs = ks + kTiles<D, BF16> * kBN * (D + 4);  // [64][D]
+  float* ps = vs + kTiles<D, BF16> * kBN * D;        // [M][64 + 4]
   auto* mem = reinterpret_cast<typename SimtSched<M>::Mem*>(ps + M * (kBN + 4));
 
   SimtSched<M> sched;
@@ -61,7 +88,37 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
   while (sched.next(&it)) {
     const int g = a.s.g, row0 = it.blk * M;
     const int past = it.r.kl - it.r.ql;  // position of the request's first new token
+    const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
+    auto load = [&](int t, int at) {  // tile t
+      float* kt = ks + at * kBN * (D + 4);
+      float* vt = vs + at * kBN * D;
+      for (int e = tid; e < kBN * D / 4; e += kThreads) {
+        const int jj = e / (D / 4), c = (e - jj * (D / 4)) * 4, j = t * kBN + jj;
+        int id = -1, off = 0;
+        if (j < it.r.kl) {
+          const int blk = a.by_bs.div(j);
+          id = __ldg(table + blk);
+          off = j - blk * a.bs;
+        }
+        const bool in = id >= 0 && id < a.num_blocks;
+        const size_t from = in ? (((size_t)id * a.bs + off) * a.s.Hkv + it.h) * D + c : 0;
+        if (BF16) {
+          float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
+          if (in) {
+            kk = ld4f<BF16>(a.kc, from);
+            vv = ld4f<BF16>(a.vc, from);
+          }
+          *reinterpret_cast<float4*>(kt + jj * (D + 4) + c) = kk;
+          *reinterpret_cast<float4*>(vt + jj * D + c) = vv;
+        } else {
+          copy16(kt + jj * (D + 4) + c, reinterpret_cast<const float*>(a.kc) + from, in);
+          copy16(vt + jj * D + c, reinterpret_cast<const float*>(a.vc) + from, in);
+        }
+      }
+      if (!BF16) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     __syncthreads();
+    if (!BF16 && it.te > it.tb) load(it.tb, 0);
     for (int e = tid; e < M * D / 4; e += kThreads) {
       const int rr = e / (D / 4), c = (e - rr * (D / 4)) * 4, row = row0 + rr;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -85,47 +142,48 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
     }
     const int pos_first = past + row0 / g;
     const int pos_last = past + (min(it.r.rows, row0 + M) - 1) / g;
-    const int32_t* table = a.s.block_tables + (size_t)it.n * a.s.max_blocks;
 
     for (int t = it.tb; t < it.te; ++t) {
-      __syncthreads();
-      for (int e = tid; e < kBN * D / 4; e += kThreads) {
-        const int jj = e / (D / 4), c = (e - jj * (D / 4)) * 4, j = t * kBN + jj;
-        float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-        if (j < it.r.kl) {
-          const int id = __ldg(table + j / a.bs);
-          if (id >= 0 && id < a.num_blocks) {
-            const size_t at = (((size_t)id * a.bs + j % a.bs) * a.s.Hkv + it.h) * D + c;
-            kk = ld4f<BF16>(a.kc, at);
-            vv = ld4f<BF16>(a.vc, at);
-          }
-        }
-        *reinterpret_cast<float4*>(ks + jj * (D + 4) + c) = kk;
-        *reinterpret_cast<float4*>(vs + jj * D + c) = vv;
+      if (BF16) {
+        __syncthreads();
+        load(t, 0);
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       __syncthreads();
+      if (!BF16 && t + 1 < it.te) load(t + 1, (t + 1 - it.tb) & 1);
+      const float* kt = ks + (BF16 ? 0 : (t - it.tb) & 1) * kBN * (D + 4);
+      const float* vt = vs + (BF16 ? 0 : (t - it.tb) & 1) * kBN * D;
       float x[R][4];
+      {
+        uint64_t x2[R][4];  // sums over even and odd columns
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[i][c] = 0.f;
+          for (int c = 0; c < 4; ++c) x2[i][c] = 0;
 #pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 kk[4];
+        for (int d = 0; d < D; d += 4) {
+          ulonglong2 kk[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          kk[c] = *reinterpret_cast<const float4*>(ks + (tx + 16 * c) * (D + 4) + d);
+          for (int c = 0; c < 4; ++c)
+            kk[c] = *reinterpret_cast<const ulonglong2*>(kt + (tx + 16 * c) * (D + 4) + d);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const float4 qq = *reinterpret_cast<const float4*>(qs + (ty * R + i) * D + d);
+          for (int i = 0; i < R; ++i) {
+            const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(qs + (ty * R + i) * D + d);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            x[i][c] = fmaf(qq.x, kk[c].x, x[i][c]);
-            x[i][c] = fmaf(qq.y, kk[c].y, x[i][c]);
-            x[i][c] = fmaf(qq.z, kk[c].z, x[i][c]);
-            x[i][c] = fmaf(qq.w, kk[c].w, x[i][c]);
+            for (int c = 0; c < 4; ++c) {
+              x2[i][c] = fma2(qq.x, kk[c].x, x2[i][c]);
+              x2[i][c] = fma2(qq.y, kk[c].y, x2[i][c]);
+            }
           }
         }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 y = halves(x2[i][c]);
+            x[i][c] = y.x + y.y;
+          }
       }
       const bool edge = t * kBN + kBN - 1 > pos_first ||
                         (a.s.window > 0 && t * kBN <= pos_last - a.s.window);
@@ -172,14 +230,23 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
 #pragma unroll
           for (int b = 0; b < NC / CV; ++b)
 #pragma unroll
-            for (int c = 0; c < CV; ++c) vv[b * CV + c] = vs[(j + u) * D + b * 16 * CV + tx * CV + c];
+            for (int c = 0; c < CV; ++c) vv[b * CV + c] = vt[(j + u) * D + b * 16 * CV + tx * CV + c];
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             const float p = u == 0 ? pp[i].x : u == 1 ? pp[i].y : u == 2 ? pp[i].z : pp[i].w;
             // a token that the row does not see adds nothing, not even 0 * inf
             if (!edge || p != 0.f) {
+              if (NC >= 2) {
+                const uint64_t p2 = pair_of(p, p);
 #pragma unroll
-              for (int c = 0; c < NC; ++c) o[i][c] = fmaf(p, vv[c], o[i][c]);
+                for (int c = 0; c + 1 < NC; c += 2) {
+                  const float2 y = halves(fma2(p2, pair_of(vv[c], vv[c + 1]), pair_of(o[i][c], o[i][c + 1])));
+                  o[i][c] = y.x;
+                  o[i][c + 1] = y.y;
+                }
+              } else {
+                o[i][0] = fmaf(p, vv[0], o[i][0]);
+              }
             }
           }
         }
@@ -216,17 +283,20 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
 
 template <int D, int M>
 cudaError_t launch_simt(const AttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
-  constexpr int bytes = simt_smem<D, M>();
   cudaError_t e;
   if (bf16) {
-    static std::atomic<unsigned long long> done{0};
-    e = ensure_smem_cap(paged_simt_kernel<D, M, true>, bytes, done);
-    if (e != cudaSuccess) return e;
-    paged_simt_kernel<D, M, true><<<grid, kThreads, bytes, stream>>>(a);
+    if constexpr (D < 64) {  // above, bf16 has kernels of its own
+      constexpr int bytes = simt_smem<D, M, true>();
+      static std::atomic<unsigned long long> done{0};
+      if ((e = ensure_smem_cap(paged_simt_kernel<D, M, true>, bytes, done)) != cudaSuccess) return e;
+      paged_simt_kernel<D, M, true><<<grid, kThreads, bytes, stream>>>(a);
+    } else {
+      return cudaErrorInvalidValue;
+    }
   } else {
+    constexpr int bytes = simt_smem<D, M, false>();
     static std::atomic<unsigned long long> done{0};
-    e = ensure_smem_cap(paged_simt_kernel<D, M, false>, bytes, done);
-    if (e != cudaSuccess) return e;
+    if ((e = ensure_smem_cap(paged_simt_kernel<D, M, false>, bytes, done)) != cudaSuccess) return e;
     paged_simt_kernel<D, M, false><<<grid, kThreads, bytes, stream>>>(a);
   }
   e = cudaGetLastError();
@@ -295,6 +365,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   AttnArgs k{};
   k.q = a.q; k.kc = a.k_cache; k.vc = a.v_cache; k.out = a.out; k.lse = a.lse;
   k.q_stride = a.q_stride; k.Hq = a.Hq; k.bs = a.block_size; k.num_blocks = a.num_blocks;
+  k.by_bs = FastDiv((unsigned)a.block_size);
   k.scale_log2 = a.scale * 1.4426950408889634f;
   k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.by_g = FastDiv((unsigned)k.s.g);
   k.s.by_hkv = FastDiv((unsigned)a.Hkv); k.s.Hkv = a.Hkv; k.s.window = a.window;

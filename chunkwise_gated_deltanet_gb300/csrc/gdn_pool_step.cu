@@ -9,11 +9,11 @@
 //
 // Bound by HBM for a few tokens (8 dk dv bytes a (request, head)), by arithmetic from about a
 // dozen on (8 dk dv operations a token).  Two kernels, chosen by the tokens a request has on
-// average, T / N (measured at 16 and 32 heads of 128, bf16; 1 to 8 tokens x 256 requests, 1 to
-// 64 tokens x 48 requests):
+// average, T / N (bf16, heads of 128; us of the one / the other):
 //
-//   up to 8   token by token on the CUDA cores           TOKENS us         183 us
-//   above     8 tokens at a time on the tensor cores     141 us            152 us
+//   up to 14  token by token on the CUDA cores    1 to 8 tokens x 256 requests of 16 heads: 98 / 141;
+//                                                  12 x 128: 100 / 114; 16 x 128: 117 / 114
+//   above     8 at a time on the tensor cores     24 x 96: 133 / 118; 1 to 64 x 48 of 32 heads: 223 / 158
 //
 // Both stage k, q, v of 8 tokens by cp.async while the 8 before are computed, and read and
 // write a unit's state, one (request, head), once.
@@ -54,7 +54,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kTok = 8;  // tokens staged at a time
+constexpr int kTok = 8;          // tokens staged at a time
+constexpr int kFewTokens = 14;   // tokens a request up to which they go one by one
 
 template <bool BF16>
 __device__ __forceinline__ void st1f(void* p, size_t i, float x) {
@@ -687,7 +688,7 @@ template <int DK, bool BF16>
 cudaError_t launch_step(const StepArgs& a, cudaStream_t stream) {
   const long long ctas = (long long)a.N * a.H;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if ((long long)a.T > (long long)kTok * a.N) {
+  if ((long long)a.T > (long long)kFewTokens * a.N) {
     step_chunks_kernel<DK, BF16><<<(unsigned)ctas, 32 * (a.dv / 16), 0, stream>>>(a);
     return cudaGetLastError();
   }

@@ -21,6 +21,7 @@ struct AttnArgs {
   float2* part_ml; // [2 CTAs][M] running maximum (log2 units) and sum
   long long q_stride;
   int Hq, bs, num_blocks;
+  FastDiv by_bs;
   float scale_log2;
   SchedArgs s;
 };

@@ -55,13 +55,14 @@ template <int D, int BN>
 struct PageLoads {
   const int32_t* table;
   int kl, h, bs, num_blocks, box;
+  FastDiv by_bs;
   __device__ PageLoads(const AttnArgs& a, const Item& it, int box_rows)
       : table(a.s.block_tables + (size_t)it.n * a.s.max_blocks), kl(it.r.kl), h(it.h), bs(a.bs),
-        num_blocks(a.num_blocks), box(box_rows) {}
+        num_blocks(a.num_blocks), box(box_rows), by_bs(a.by_bs) {}
   // Page and group of box `e` of tile `t` (BN / box <= 16 boxes: a lane each).
   __device__ __forceinline__ int2 page(int t, int e) const {
     const int j = t * BN + e * box;
-    const int blk = j / bs;
+    const int blk = by_bs.div(j);
     const int id = e * box < BN && j < kl ? __ldg(table + blk) : -1;
     return make_int2(id >= 0 && id < num_blocks ? id : num_blocks, (j - blk * bs) >> 3);
   }
