@@ -69,7 +69,7 @@ __device__ __forceinline__ float4 ld4f(const void* p, size_t i) {
 // score product each lane has 4 keys (16 apart), in the value product D / 16 columns.  K
 // rows are padded by 4 floats so that the lanes' float4 reads fall into different banks.
 template <int D, int M, bool BF16>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, D <= 64 ? 2 : 1) paged_simt_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int R = M / 16;                   // rows a thread
   constexpr int NC = D / 16;                  // output columns a thread
   constexpr int CV = NC >= 4 ? 4 : NC;        // of them, consecutive
@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const AttnArgs a) 
   float* ps = vs + kTiles<D, BF16> * kBN * D;        // [M][64 + 4]
   auto* mem = reinterpret_cast<typename SimtSched<M>::Mem*>(ps + M * (kBN + 4));
 
+  after_previous_kernel();
   SimtSched<M> sched;
   sched.template init<kThreads>(a.s, mem, blockIdx.x, gridDim.x);
   let_next_kernel_start();
@@ -288,18 +289,17 @@ cudaError_t launch_simt(const AttnArgs& a, bool bf16, int grid, cudaStream_t str
     if constexpr (D < 64) {  // above, bf16 has kernels of its own
       constexpr int bytes = simt_smem<D, M, true>();
       static std::atomic<unsigned long long> done{0};
-      if ((e = ensure_smem_cap(paged_simt_kernel<D, M, true>, bytes, done)) != cudaSuccess) return e;
-      paged_simt_kernel<D, M, true><<<grid, kThreads, bytes, stream>>>(a);
+      if ((e = ensure_smem_cap(paged_simt_kernel<D, M, true>, bytes, done, true)) != cudaSuccess) return e;
+      e = launch_early(paged_simt_kernel<D, M, true>, dim3(grid), kThreads, bytes, stream, a);
     } else {
       return cudaErrorInvalidValue;
     }
   } else {
     constexpr int bytes = simt_smem<D, M, false>();
     static std::atomic<unsigned long long> done{0};
-    if ((e = ensure_smem_cap(paged_simt_kernel<D, M, false>, bytes, done)) != cudaSuccess) return e;
-    paged_simt_kernel<D, M, false><<<grid, kThreads, bytes, stream>>>(a);
+    if ((e = ensure_smem_cap(paged_simt_kernel<D, M, false>, bytes, done, true)) != cudaSuccess) return e;
+    e = launch_early(paged_simt_kernel<D, M, false>, dim3(grid), kThreads, bytes, stream, a);
   }
-  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_join<D, SimtSched<M>>(a, bf16, grid, stream);
 }
@@ -315,6 +315,8 @@ cudaError_t launch_simt_d(const AttnArgs& a, int d, bool bf16, int grid, cudaStr
   }
 }
 
+// As many CTAs as the SMs hold, so that each SM has its share wherever they are placed.
+int simt_grid(int d) { return sm_count() * (d <= 64 ? 2 : 1); }
 size_t part_bytes(int grid, int M, int d) { return (size_t)2 * grid * M * (d + 2) * 4; }
 
 }  // namespace
@@ -338,7 +340,7 @@ Plan plan_of(int bf16, int d, long long rows) {
 size_t paged_attn_workspace_bytes(int Hq, int Hkv, int d, int bf16, int max_q_len) {
   const int grid = sm_count();
   const Plan p = plan_of(bf16, d, (long long)max_q_len * (Hq / Hkv));
-  if (p.simt) return part_bytes(grid, p.simt, d);
+  if (p.simt) return part_bytes(simt_grid(d), p.simt, d);
   return std::max(paged_mma_part_bytes(d), p.tc ? paged_tc_part_bytes(grid, d) : 0);
 }
 
@@ -361,7 +363,7 @@ bool paged_attn_fits(const PagedAttnArgs& a) {
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
   const Plan p = plan_of(a.bf16, a.d, (long long)a.max_q_len * (a.Hq / a.Hkv));
-  const int grid = sm_count();
+  const int grid = p.simt ? simt_grid(a.d) : sm_count();
   AttnArgs k{};
   k.q = a.q; k.kc = a.k_cache; k.vc = a.v_cache; k.out = a.out; k.lse = a.lse;
   k.q_stride = a.q_stride; k.Hq = a.Hq; k.bs = a.block_size; k.num_blocks = a.num_blocks;

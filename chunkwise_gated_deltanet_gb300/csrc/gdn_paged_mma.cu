@@ -385,6 +385,7 @@ paged_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     prefetch_tensormap(&mk);
     prefetch_tensormap(&mv);
   }
+  after_previous_kernel();
   MmSched sched;
   sched.template init<kMmThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);  // ends in a barrier
   let_next_kernel_start();
@@ -421,8 +422,9 @@ cudaError_t launch_mma(AttnArgs a, cudaStream_t stream) {
   const int grid = mma_grid();
   a.s.unit_cost = 2;  // a unit's start and join take about as long as two tiles
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kMmM * D);
-  paged_mma_kernel<D><<<grid, kMmThreads, bytes, stream>>>(a, mk, mv, box, status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_early(paged_mma_kernel<D>, dim3(grid), kMmThreads, bytes, stream, a, mk, mv, box, status)) !=
+      cudaSuccess)
+    return e;
   return launch_join<D, MmSched>(a, true, grid, stream);
 }
 

@@ -3,6 +3,7 @@
 // cache (gdn_paged_write).
 #include <cuda_runtime.h>
 
+#include "early_launch.cuh"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -54,12 +55,14 @@ __device__ __forceinline__ int sat32(long long x) {
   return x > 0x7fffffffLL ? 0x7fffffff : (int)x;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
   __shared__ int tok0[kPlanChunk + 1], need0[kPlanChunk + 1], back0[kPlanChunk + 1];
   __shared__ unsigned char ok[kPlanChunk];
   __shared__ Sum3 wsum[kPlanThreads / 32];
   __shared__ int taken_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_next_kernel_start();
+  after_previous_kernel();
   const long long cap = (long long)a.max_blocks * a.block_size;
   const int bs = a.block_size, nb = a.num_blocks;
   int head = a.ring_in[0] % nb;
@@ -201,6 +204,8 @@ paged_write_kernel(const uint8_t* __restrict__ k, const uint8_t* __restrict__ v,
                    const int32_t* __restrict__ slot_map, uint8_t* __restrict__ kc,
                    uint8_t* __restrict__ vc, long long k_stride, long long v_stride,
                    unsigned row_vecs, long long total, long long slots) {
+  let_next_kernel_start();
+  after_previous_kernel();
   const long long base = (long long)blockIdx.x * (kWriteThreads * kWriteVecs) + threadIdx.x;
   uint4 kk[kWriteVecs], vv[kWriteVecs];
   long long to[kWriteVecs];
@@ -246,8 +251,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   const int most = 2 * sm_count();
   if (ctas > most) ctas = most;
   if (ctas < 1) ctas = 1;
-  paged_plan_kernel<<<(unsigned)ctas, kPlanThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(paged_plan_kernel, dim3((unsigned)ctas), kPlanThreads, 0, stream, a);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, cudaStream_t stream) {
@@ -256,10 +260,9 @@ cudaError_t launch_paged_write(const WriteArgs& a, cudaStream_t stream) {
   const long long total = (long long)a.T * row_vecs;
   const long long ctas = (total + kWriteThreads * kWriteVecs - 1) / (kWriteThreads * kWriteVecs);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  paged_write_kernel<<<(unsigned)ctas, kWriteThreads, 0, stream>>>(
-      (const uint8_t*)a.k, (const uint8_t*)a.v, a.slot_map, (uint8_t*)a.k_cache,
-      (uint8_t*)a.v_cache, a.k_stride, a.v_stride, row_vecs, total, a.slots);
-  return cudaGetLastError();
+  return launch_early(paged_write_kernel, dim3((unsigned)ctas), kWriteThreads, 0, stream, (const uint8_t*)a.k,
+                      (const uint8_t*)a.v, a.slot_map, (uint8_t*)a.k_cache, (uint8_t*)a.v_cache, a.k_stride,
+                      a.v_stride, row_vecs, total, a.slots);
 }
 
 }  // namespace gdn

@@ -601,6 +601,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
     prefetch_tensormap(&mk);
     prefetch_tensormap(&mv);
   }
+  after_previous_kernel();
   TcSched sched;
   sched.template init<kTcThreads>(a.s, &sm.sched, blockIdx.x, gridDim.x);
   let_next_kernel_start();
@@ -649,8 +650,9 @@ cudaError_t launch_tc_d(const AttnArgs& a, int grid, cudaStream_t stream) {
   if (!make_page_map(&mk, a.kc, a.num_blocks, a.bs, a.s.Hkv, D, box) ||
       !make_page_map(&mv, a.vc, a.num_blocks, a.bs, a.s.Hkv, D, box))
     return cudaErrorInvalidValue;
-  paged_tc_kernel<D><<<grid, kTcThreads, bytes, stream>>>(a, mk, mv, box, status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_early(paged_tc_kernel<D>, dim3(grid), kTcThreads, bytes, stream, a, mk, mv, box, status)) !=
+      cudaSuccess)
+    return e;
   return launch_join<D, TcSched>(a, true, grid, stream);
 }
 

@@ -48,6 +48,7 @@
 
 #include <type_traits>
 
+#include "early_launch.cuh"
 #include "gdn_internal.h"
 #include "tc_common.cuh"
 
@@ -293,6 +294,8 @@ __global__ void __launch_bounds__(256, 2) step_tokens_kernel(const __grid_consta
     take_cta(&sm.taken, &sm.taken_full);
   }
   __syncthreads();
+  let_next_kernel_start();
+  after_previous_kernel();
   StepUnit now = first_unit(a);
   begin(now);
   if (tid == 0) look_up(0);
@@ -522,6 +525,8 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
   __shared__ ChunkSmem<DK, BF16> sm;
   using El = typename StepRaw<DK, BF16>::El;
 
+  let_next_kernel_start();
+  after_previous_kernel();
   const StepUnit now = first_unit(a);
   const int h = now.h, t0 = now.t0, t1 = now.t1;
   if (t0 == t1) return;  // no tokens: the state stays as it is
@@ -689,8 +694,7 @@ cudaError_t launch_step(const StepArgs& a, cudaStream_t stream) {
   const long long ctas = (long long)a.N * a.H;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   if ((long long)a.T > (long long)kFewTokens * a.N) {
-    step_chunks_kernel<DK, BF16><<<(unsigned)ctas, 32 * (a.dv / 16), 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_early(step_chunks_kernel<DK, BF16>, dim3((unsigned)ctas), 32 * (a.dv / 16), 0, stream, a);
   }
   int* status = nullptr;
   cudaError_t e = tc_status_address(&status);
@@ -698,8 +702,7 @@ cudaError_t launch_step(const StepArgs& a, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   if ((e = ensure_smem_cap(step_tokens_kernel<DK, BF16>, DK * 128 * 4, done, true)) != cudaSuccess) return e;
   const int threads = 32 * ((a.dv + kTokenRows<DK> - 1) / kTokenRows<DK>);
-  step_tokens_kernel<DK, BF16><<<(unsigned)ctas, threads, DK * a.dv * 4, stream>>>(a, status);
-  return cudaGetLastError();
+  return launch_early(step_tokens_kernel<DK, BF16>, dim3((unsigned)ctas), threads, DK * a.dv * 4, stream, a, status);
 }
 template <int DK>
 cudaError_t launch_dk(const StepArgs& a, cudaStream_t stream) {

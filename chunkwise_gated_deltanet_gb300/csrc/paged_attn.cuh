@@ -7,6 +7,7 @@
 
 #include <algorithm>
 
+#include "early_launch.cuh"
 #include "paged_sched.cuh"
 
 namespace gdn {
@@ -38,15 +39,6 @@ int paged_tc_requests();
 cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream);
 
 namespace {
-
-// A kernel launched to overlap the end of the one before it: wait for that one's results
-// (before), and let the next one start (in the one before).
-__device__ __forceinline__ void after_previous_kernel() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void let_next_kernel_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 __device__ __forceinline__ float lse_of(float m, float l) {
   return m == -INFINITY ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
@@ -94,19 +86,25 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   __shared__ float l_s[kJoinWarps][32];
   SCHED sched;
   sched.template init<kJoinThreads>(a.s, &mem, 0, grid);
+  let_next_kernel_start();
   const int c = blockIdx.x + 1;
-  if (c >= sched.G) return;
-  const int b = sched.share(c);
-  if (b >= sched.total) return;
-  sched.locate(b);
-  const int u0 = sched.unit0, u1 = u0 + sched.cost(sched.r, sched.blk);
-  if (b <= u0 + sched.s.unit_cost) return;  // cuts nothing: the unit is the later share's
-  int c0 = sched.share_of(u0);
-  while (sched.share(c0 + 1) <= u0 + sched.s.unit_cost) ++c0;
-  const int c1 = sched.share_of(u1 - 1);  // shares c0 .. c1 hold a part
-  // part 0 is in slot0, part i in slot 2 (c0 + i)
-  const int parts = c1 - c0 + 1, slot0 = 2 * c0 + (u0 > sched.share(c0) ? 1 : 0);
+  // the unit that boundary c cuts, and the shares c0 .. c1 that hold a part of it
+  int c0 = 0, c1 = 0, slot0 = 0;
+  const int b = c < sched.G ? sched.share(c) : sched.total;
+  if (b < sched.total) {
+    sched.locate(b);
+    const int u0 = sched.unit0, u1 = u0 + sched.cost(sched.r, sched.blk);
+    if (b > u0 + sched.s.unit_cost) {  // else it cuts nothing: the unit is the later share's
+      c0 = sched.share_of(u0);
+      while (sched.share(c0 + 1) <= u0 + sched.s.unit_cost) ++c0;
+      c1 = sched.share_of(u1 - 1);
+      // part 0 is in slot0, part i in slot 2 (c0 + i)
+      slot0 = 2 * c0 + (u0 > sched.share(c0) ? 1 : 0);
+    }
+  }
   after_previous_kernel();
+  const int parts = c1 - c0 + 1;
+  if (parts < 2) return;
   // A warp has a pair of rows, whose pieces of 16 bytes lie side by side: lane, row lane & 1 of
   // the pair and columns 4 (lane / 2 + 16 j) .. + 3.
   constexpr int NJ = (D + 63) / 64;
@@ -181,22 +179,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   }
 }
 
-// Queued behind the kernel that leaves the parts so that it starts, and reads the schedule,
-// while that one ends (it waits for it before it reads a part).
+// Starts under the end of the kernel that leaves the parts, and reads the schedule meanwhile
+// (its inputs are older than that kernel).
 template <int D, typename SCHED>
 cudaError_t launch_join(const AttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
   if (grid < 2) return cudaSuccess;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid - 1, std::max(1, SCHED::kM / 64));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return bf16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, SCHED, true>, a, grid)
-              : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, SCHED, false>, a, grid);
+  const dim3 ctas(grid - 1, std::max(1, SCHED::kM / 64));
+  return bf16 ? launch_early(paged_join_kernel<D, SCHED, true>, ctas, kJoinThreads, 0, stream, a, grid)
+              : launch_early(paged_join_kernel<D, SCHED, false>, ctas, kJoinThreads, 0, stream, a, grid);
 }
 
 }  // namespace
