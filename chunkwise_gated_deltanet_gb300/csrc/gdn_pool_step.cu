@@ -38,11 +38,11 @@
 //     S   = gamma_7 S0 + sum_s D_7s u_s k_s^T
 //
 // The products with S0 and the update run on mma.sync (m16n8k8, TF32) in three passes of
-// two-part operands (hi hi + hi lo + lo hi, about 2^-22 relative, fp32 sums); the sums over
-// s < t are eight steps in registers.  A warp has 16 rows of S in the accumulators' layout for
+// two-part operands (hi hi + hi lo + lo hi, about 2^-23 relative, fp32 sums), two where k and q
+// are bf16, which TF32 holds exactly; the sums over s < t are eight steps in registers.  A warp has 16 rows of S in the accumulators' layout for
 // the whole call.  The same registers are the products' left operand: an accumulator's columns
 // 2 t and 2 t + 1 stand for the operand's t and t + 4, and the right operands are laid out in
-// shared memory in that order, a 16-byte piece a lane (hi and lo of both values).
+// shared memory in that order, a piece a lane (hi, and lo where there is one, of both values).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -77,15 +77,29 @@ __device__ __forceinline__ void st4f(void* p, size_t i, float4 x) {
   }
 }
 
-// x = hi + lo with hi of TF32's 11 significant bits; lo is cut to them by the product.
-__device__ __forceinline__ uint32_t tf_hi(float x) { return __float_as_uint(x) & 0xffffe000u; }
+// x = hi + lo with hi rounded to TF32's 11 significant bits; lo is cut to them by the product.
+__device__ __forceinline__ uint32_t tf_hi(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ uint32_t tf_lo(float x, uint32_t hi) {
   return __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
-__device__ __forceinline__ uint4 tf_pair(float a, float b) {  // hi, hi, lo, lo
-  const uint32_t ha = tf_hi(a), hb = tf_hi(b);
-  return make_uint4(ha, hb, tf_lo(a, ha), tf_lo(b, hb));
-}
+// A right operand's two values: bf16 as they are; fp32 as hi, hi, lo, lo.
+template <bool BF16>
+struct Right;
+template <>
+struct Right<true> {
+  uint2 hi;
+  __device__ __forceinline__ static Right of(float a, float b) {
+    return Right{make_uint2(__float_as_uint(a), __float_as_uint(b))};
+  }
+};
+template <>
+struct Right<false> {
+  uint2 hi, lo;
+  __device__ __forceinline__ static Right of(float a, float b) {
+    const uint32_t ha = tf_hi(a), hb = tf_hi(b);
+    return Right{make_uint2(ha, hb), make_uint2(tf_lo(a, ha), tf_lo(b, hb))};
+  }
+};
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -93,11 +107,26 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c += a b in three passes; b as tf_pair has it.
-__device__ __forceinline__ void mma_3(float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint4 b) {
-  mma_tf32(c, lo, b.x, b.y);
-  mma_tf32(c, hi, b.z, b.w);
-  mma_tf32(c, hi, b.x, b.y);
+// c += a b in three passes, or two.
+__device__ __forceinline__ void mma_parts(float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                          const Right<false>& b) {
+  mma_tf32(c, lo, b.hi.x, b.hi.y);
+  mma_tf32(c, hi, b.lo.x, b.lo.y);
+  mma_tf32(c, hi, b.hi.x, b.hi.y);
+}
+__device__ __forceinline__ void mma_parts(float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                          const Right<true>& b) {
+  mma_tf32(c, lo, b.hi.x, b.hi.y);
+  mma_tf32(c, hi, b.hi.x, b.hi.y);
+}
+// c += [k; q] k^T of two pieces
+__device__ __forceinline__ void mma_tokens(float (&c)[4], const Right<false>& k, const Right<false>& q) {
+  const uint32_t hi[4] = {k.hi.x, q.hi.x, k.hi.y, q.hi.y}, lo[4] = {k.lo.x, q.lo.x, k.lo.y, q.lo.y};
+  mma_parts(c, hi, lo, k);
+}
+__device__ __forceinline__ void mma_tokens(float (&c)[4], const Right<true>& k, const Right<true>& q) {
+  const uint32_t hi[4] = {k.hi.x, q.hi.x, k.hi.y, q.hi.y};
+  mma_tf32(c, hi, k.hi.x, k.hi.y);
 }
 
 // 16 or 4 bytes into shared memory, zeros where there are none.
@@ -505,7 +534,7 @@ struct ChunkSmem {
   StepRaw<DK, BF16> raw;
   // right operands, a piece a lane (g = lane / 4, t = lane % 4) and 8 columns: k and q of token
   // g at the columns of the lane's accumulators, and k of tokens 2 t, 2 t + 1 at column g's
-  alignas(16) uint4 kd[DK / 8][32], qd[DK / 8][32], ku[DK / 8][32];
+  alignas(16) Right<BF16> kd[DK / 8][32], qd[DK / 8][32], ku[DK / 8][32];
   // of tokens 2 t, 2 t + 1 and s: beta_t D_ts k_t . k_s (s < t, else 0) of both, D_ts q_t . k_s
   // (s <= t) of both
   alignas(16) float4 m[kTok][4];
@@ -562,9 +591,9 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
     auto f = [](El x) { return (float)x; };
     for (int e = tid; e < NT * 32; e += nthreads) {
       const int m = e >> 5, lg = (e & 31) >> 2, lt = e & 3, c = col_of(m, 2 * lt), cg = col_of(m, lg);
-      sm.kd[m][e & 31] = tf_pair(f(sm.raw.k[lg][c]), f(sm.raw.k[lg][c + 1]));
-      sm.qd[m][e & 31] = tf_pair(f(sm.raw.q[lg][c]), f(sm.raw.q[lg][c + 1]));
-      sm.ku[m][e & 31] = tf_pair(f(sm.raw.k[2 * lt][cg]), f(sm.raw.k[2 * lt + 1][cg]));
+      sm.kd[m][e & 31] = Right<BF16>::of(f(sm.raw.k[lg][c]), f(sm.raw.k[lg][c + 1]));
+      sm.qd[m][e & 31] = Right<BF16>::of(f(sm.raw.q[lg][c]), f(sm.raw.q[lg][c + 1]));
+      sm.ku[m][e & 31] = Right<BF16>::of(f(sm.raw.k[2 * lt][cg]), f(sm.raw.k[2 * lt + 1][cg]));
     }
     for (int e = tid; e < kTok * kTok; e += nthreads) {
       const int i = e >> 3, j = e & 7;  // D_ij, and in the row's end gamma_j and D_7j
@@ -593,9 +622,7 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
     {
       float c[4] = {0.f, 0.f, 0.f, 0.f};
       for (int m = warp; m < NT; m += nwarps) {
-        const uint4 kk = sm.kd[m][lane], qq = sm.qd[m][lane];
-        const uint32_t hi[4] = {kk.x, qq.x, kk.y, qq.y}, lo[4] = {kk.z, qq.z, kk.w, qq.w};
-        mma_3(c, hi, lo, kk);
+        mma_tokens(c, sm.kd[m][lane], sm.qd[m][lane]);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) sm.part[warp][g + 8 * (e >> 1)][2 * t + (e & 1)] = c[e];
@@ -628,8 +655,8 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
         hi[e] = tf_hi(x[e]);
         lo[e] = tf_lo(x[e], hi[e]);
       }
-      mma_3(p[m & 1], hi, lo, sm.kd[m][lane]);
-      mma_3(o[m & 1], hi, lo, sm.qd[m][lane]);
+      mma_parts(p[m & 1], hi, lo, sm.kd[m][lane]);
+      mma_parts(o[m & 1], hi, lo, sm.qd[m][lane]);
     }
     __syncthreads();  // m is there
     float u[2][2], y[2][2];
@@ -678,7 +705,7 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
     for (int m = 0; m < NT; ++m) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[m][e] *= gamma;
-      mma_3(s[m], hi, lo, sm.ku[m][lane]);
+      mma_parts(s[m], hi, lo, sm.ku[m][lane]);
     }
   }
 #pragma unroll
