@@ -529,19 +529,24 @@ __global__ void __launch_bounds__(256, 2) step_tokens_kernel(const __grid_consta
   }
 }
 
+// What a chunk's products use; two, so that the next chunk's is made under this one's.
 template <int DK, bool BF16>
-struct ChunkSmem {
-  StepRaw<DK, BF16> raw;
+struct ChunkOperands {
   // right operands, a piece a lane (g = lane / 4, t = lane % 4) and 8 columns: k and q of token
   // g at the columns of the lane's accumulators, and k of tokens 2 t, 2 t + 1 at column g's
   alignas(16) Right<BF16> kd[DK / 8][32], qd[DK / 8][32], ku[DK / 8][32];
   // of tokens 2 t, 2 t + 1 and s: beta_t D_ts k_t . k_s (s < t, else 0) of both, D_ts q_t . k_s
   // (s <= t) of both
   alignas(16) float4 m[kTok][4];
-  float decay[kTok][kTok];      // D_ts
-  float part[8][16][kTok + 1];  // a warp's part of k_i . k_j (rows 0-7) and q_i . k_j (8-15)
+  float decay[kTok][kTok];  // D_ts
   float beta[kTok], gamma[kTok], last[kTok];
 };
+template <int DK, bool BF16>
+struct ChunkSmem {
+  StepRaw<DK, BF16> raw;
+  ChunkOperands<DK, BF16> op[2];
+};
+
 // Column of an accumulator's entry: tile n of 8, column j of the tile.  A lane's entries of
 // tiles 2 m and 2 m + 1 are the four consecutive columns 16 m + 4 t ..
 __device__ __forceinline__ int col_of(int n, int j) {
@@ -551,7 +556,8 @@ __device__ __forceinline__ int col_of(int n, int j) {
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_constant__ StepArgs a) {
   constexpr int NT = DK / 8;  // column tiles of S
-  __shared__ ChunkSmem<DK, BF16> sm;
+  extern __shared__ __align__(16) uint8_t chunk_smem[];
+  auto& sm = *reinterpret_cast<ChunkSmem<DK, BF16>*>(chunk_smem);
   using El = typename StepRaw<DK, BF16>::El;
 
   let_next_kernel_start();
@@ -583,64 +589,62 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
       s[m + 1][2 * r + 1] = x.w;
     }
 
-  for (int tb = t0; tb < t1; tb += kTok) {
-    const int nt = min(kTok, t1 - tb);
-    landed();
-    __syncthreads();
-    // from the staged tokens: the operands, the gates, and v of this lane's rows
+  float v[2][2];  // of rows row, row + 8 and tokens 2 t, 2 t + 1
+  // from the staged tokens: the operands, the gates, and v of this lane's rows
+  auto make = [&](ChunkOperands<DK, BF16>& op) {
     auto f = [](El x) { return (float)x; };
     for (int e = tid; e < NT * 32; e += nthreads) {
       const int m = e >> 5, lg = (e & 31) >> 2, lt = e & 3, c = col_of(m, 2 * lt), cg = col_of(m, lg);
-      sm.kd[m][e & 31] = Right<BF16>::of(f(sm.raw.k[lg][c]), f(sm.raw.k[lg][c + 1]));
-      sm.qd[m][e & 31] = Right<BF16>::of(f(sm.raw.q[lg][c]), f(sm.raw.q[lg][c + 1]));
-      sm.ku[m][e & 31] = Right<BF16>::of(f(sm.raw.k[2 * lt][cg]), f(sm.raw.k[2 * lt + 1][cg]));
+      op.kd[m][e & 31] = Right<BF16>::of(f(sm.raw.k[lg][c]), f(sm.raw.k[lg][c + 1]));
+      op.qd[m][e & 31] = Right<BF16>::of(f(sm.raw.q[lg][c]), f(sm.raw.q[lg][c + 1]));
+      op.ku[m][e & 31] = Right<BF16>::of(f(sm.raw.k[2 * lt][cg]), f(sm.raw.k[2 * lt + 1][cg]));
     }
     for (int e = tid; e < kTok * kTok; e += nthreads) {
-      const int i = e >> 3, j = e & 7;  // D_ij, and in the row's end gamma_j and D_7j
+      const int i = e >> 3, j = e & 7;  // D_ij, and with the last row gamma_j and D_7j
       float x = 0.f;
       for (int u = j + 1; u <= i; ++u) x += sm.raw.la[u];
-      sm.decay[i][j] = j > i ? 0.f : expf(x);
+      op.decay[i][j] = j > i ? 0.f : expf(x);
       if (i == kTok - 1) {
-        sm.last[j] = expf(x);
+        op.last[j] = expf(x);
         float y = 0.f;
         for (int u = 0; u <= j; ++u) y += sm.raw.la[u];
-        sm.gamma[j] = expf(y);
-        sm.beta[j] = sm.raw.beta[j];
+        op.gamma[j] = expf(y);
+        op.beta[j] = sm.raw.beta[j];
       }
     }
-    float v[2][2];  // tokens 2 t, 2 t + 1 (second index)
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int b = 0; b < 2; ++b) v[r][b] = f(sm.raw.v[2 * t + b][row + 8 * r]);
-    __syncthreads();
-    if (tb + kTok < t1) {
+  };
+  landed();
+  __syncthreads();
+  make(sm.op[0]);
+  __syncthreads();
+
+  for (int tb = t0, i = 0; tb < t1; tb += kTok, ++i) {
+    const int nt = min(kTok, t1 - tb);
+    const bool more = tb + kTok < t1;
+    auto& op = sm.op[i & 1];
+    if (more) {
       stage(sm.raw, a, now, tb + kTok);
       commit();
     }
-    // the tokens' products with each other: a warp takes every (warps)-th tile of columns
-    {
+    if (warp == i % nwarps) {  // the tokens' products with each other, by the warps in turn
       float c[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int m = warp; m < NT; m += nwarps) {
-        mma_tokens(c, sm.kd[m][lane], sm.qd[m][lane]);
-      }
+#pragma unroll 4
+      for (int m = 0; m < NT; ++m) mma_tokens(c, op.kd[m][lane], op.qd[m][lane]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sm.part[warp][g + 8 * (e >> 1)][2 * t + (e & 1)] = c[e];
+      for (int e = 0; e < 4; ++e) {
+        const int j = 2 * t + (e & 1);  // k_g . k_j, then q_g . k_j
+        const float x = j > g ? 0.f : op.decay[g][j] * c[e];
+        float* to = reinterpret_cast<float*>(&op.m[j][g >> 1]) + (g & 1);
+        if (e < 2)
+          to[0] = j < g ? op.beta[g] * x : 0.f;
+        else
+          to[2] = x;
+      }
     }
-    __syncthreads();
-    for (int e = tid; e < 2 * kTok * kTok; e += nthreads) {
-      const int i = e >> 3, j = e & 7;  // row i of part, token j
-      const int ti = i & 7;
-      float dot = 0.f;
-      for (int w = 0; w < min(nwarps, NT); ++w) dot += sm.part[w][i][j];
-      float* to = reinterpret_cast<float*>(&sm.m[j][ti >> 1]) + (ti & 1);
-      const float x = j > ti ? 0.f : sm.decay[ti][j] * dot;
-      if (i >= kTok)
-        to[2] = x;
-      else
-        to[0] = j < ti ? sm.beta[ti] * x : 0.f;
-    }
-
     float p[2][4], o[2][4];  // S0 k and S0 q of the 16 rows and 8 tokens, in two chains each
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -655,14 +659,15 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
         hi[e] = tf_hi(x[e]);
         lo[e] = tf_lo(x[e], hi[e]);
       }
-      mma_parts(p[m & 1], hi, lo, sm.kd[m][lane]);
-      mma_parts(o[m & 1], hi, lo, sm.qd[m][lane]);
+      mma_parts(p[m & 1], hi, lo, op.kd[m][lane]);
+      mma_parts(o[m & 1], hi, lo, op.qd[m][lane]);
     }
-    __syncthreads();  // m is there
+    landed();
+    __syncthreads();  // m is there, and the next chunk's tokens
     float u[2][2], y[2][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const float beta = sm.beta[2 * t + b], gamma = sm.gamma[2 * t + b];
+      const float beta = op.beta[2 * t + b], gamma = op.gamma[2 * t + b];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         u[r][b] = beta * fmaf(-gamma, p[0][2 * r + b] + p[1][2 * r + b], v[r][b]);
@@ -671,7 +676,7 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const float4 m = sm.m[j][t];
+      const float4 m = op.m[j][t];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float x = __shfl_sync(0xffffffffu, u[r][j & 1], (lane & ~3) + (j >> 1));
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const float w = sm.last[2 * t + b];
+      const float w = op.last[2 * t + b];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float x = w * u[r][b];
@@ -700,12 +705,16 @@ __global__ void __launch_bounds__(256, 2) step_chunks_kernel(const __grid_consta
         lo[2 * b + r] = tf_lo(x, hi[2 * b + r]);
       }
     }
-    const float gamma = sm.gamma[kTok - 1];
+    const float gamma = op.gamma[kTok - 1];
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[m][e] *= gamma;
-      mma_parts(s[m], hi, lo, sm.ku[m][lane]);
+      mma_parts(s[m], hi, lo, op.ku[m][lane]);
+    }
+    if (more) {
+      make(sm.op[(i + 1) & 1]);
+      __syncthreads();  // the operands are there, and the staged tokens used
     }
   }
 #pragma unroll
@@ -720,12 +729,15 @@ template <int DK, bool BF16>
 cudaError_t launch_step(const StepArgs& a, cudaStream_t stream) {
   const long long ctas = (long long)a.N * a.H;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaError_t e;
   if ((long long)a.T > (long long)kFewTokens * a.N) {
-    return launch_early(step_chunks_kernel<DK, BF16>, dim3((unsigned)ctas), 32 * (a.dv / 16), 0, stream, a);
+    constexpr int bytes = (int)sizeof(ChunkSmem<DK, BF16>);
+    static std::atomic<unsigned long long> done{0};
+    if ((e = ensure_smem_cap(step_chunks_kernel<DK, BF16>, bytes, done, true)) != cudaSuccess) return e;
+    return launch_early(step_chunks_kernel<DK, BF16>, dim3((unsigned)ctas), 32 * (a.dv / 16), bytes, stream, a);
   }
   int* status = nullptr;
-  cudaError_t e = tc_status_address(&status);
-  if (e != cudaSuccess) return e;
+  if ((e = tc_status_address(&status)) != cudaSuccess) return e;
   static std::atomic<unsigned long long> done{0};
   if ((e = ensure_smem_cap(step_tokens_kernel<DK, BF16>, DK * 128 * 4, done, true)) != cudaSuccess) return e;
   const int threads = 32 * ((a.dv + kTokenRows<DK> - 1) / kTokenRows<DK>);
