@@ -76,6 +76,8 @@ def _step(lib, **over):
     (_attend, dict(lse=A[7] + 2), 1, "lse"), (_attend, dict(qs=508), 1, "q_stride"),
     (_attend, dict(qs=516), 1, "q_stride"), (_attend, dict(ws=None), 1, "workspace"),
     (_attend, dict(wb=64), 1, "workspace holds 64"),
+    (_attend, dict(M=(1 << 21) - 2, bs=1024, T=1 << 27, mq=1 << 27), 1, "max_seq_len"),
+    (_attend, dict(M=(1 << 21) - 2, bs=1024, T=1 << 27, mq=1 << 27, d=32, qs=256, dt=0), 1, "max_seq_len"),
     (_step, dict(dt=3), 2, "qkv_dtype"), (_step, dict(N=-1), 1, "N, T"), (_step, dict(slots=0), 1, "slots"),
     (_step, dict(H=3), 1, "multiple of Hk"), (_step, dict(dk=48), 1, "dk and dv"), (_step, dict(dv=256), 1, "dk and dv"),
     (_step, dict(sp=None), 1, "state_pool"), (_step, dict(sp=A[5] + 4), 1, "16-byte"), (_step, dict(la=None), 1, "log_alpha"),

@@ -527,3 +527,69 @@ def test_step_bad_tokens_reach_later_ones_only(dtype):
     bad = run(v, k2)
     assert torch.equal(bad[:5], good[:5]) and torch.equal(bad[7:], good[7:]) and torch.equal(bad[:, 0], good[:, 0])
     assert torch.isnan(bad[5:7, 1]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("most", [3, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_step_more_units_than_the_gpu_holds(d, most, dtype):
+    """Requests without tokens, new ones and slots out of range in between, token by token and
+    in chunks; 800 (request, head) pairs."""
+    N, H = 200, 4
+    g = torch.Generator().manual_seed(most + d)
+    lens = torch.randint(0, most + 1, (N,), generator=g).tolist()
+    q, k, v, la, beta, pool, index, ctx = _step_inputs(lens, 2, H, d, d, dtype, 21, fresh=range(0, N, 7))
+    gone = list(range(3, N, 11))
+    index[gone[::2]], index[gone[1::2]] = -1, pool.shape[0]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    pd = pool.to(DEV)
+    out = gdn.recurrent_step(*(x.to(DEV) for x in (q, k, v, la, beta)), pd, index.to(DEV), _i32(cu),
+                             context_lens=ctx.to(DEV)).double().cpu().numpy()
+    want, ref = pool.double().numpy().copy(), np.zeros(out.shape)
+    for n, L in enumerate(lens):
+        if L == 0 or n in gone:
+            continue
+        sl = slice(cu[n], cu[n + 1])
+        S0 = pool[index[n]][None] * float(ctx[n] > 0)
+        o, S = native.gdn_forward_c(q[None, sl].repeat_interleave(2, 2).contiguous(),
+                                    k[None, sl].repeat_interleave(2, 2).contiguous(), v[None, sl].contiguous(),
+                                    la[None, sl].contiguous(), beta[None, sl].contiguous(), S0.contiguous(), None)
+        ref[sl], want[int(index[n])] = o[0], S[0]
+    slack = 2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0.0
+    assert (np.abs(out - ref) - slack).max() <= TOL_F32_REL_MAX * np.abs(ref).max()
+    assert np.abs(pd.double().cpu().numpy() - want).max() <= TOL_F32_REL_MAX * np.abs(want).max()
+    for n in gone:
+        assert (out[cu[n]:cu[n + 1]] == 0).all()
+    still = [int(index[n]) for n in range(N) if lens[n] == 0 and n not in gone]
+    assert torch.equal(pd.cpu()[still], pool[still])
+
+
+@pytest.mark.parametrize("lens", [[3, 1, 0, 6], [40, 17]])
+def test_plan_write_and_step_on_another_stream(lens):
+    """Inputs that a side stream is still writing when the calls are made on it."""
+    N, T, bs = len(lens), sum(lens), 16
+    q, k, v, la, beta, pool, index, _ = _step_inputs(lens, 2, 2, 64, 64, "bf16", 31)
+    host = [x.pin_memory() for x in (q, k, v, la, beta, pool, index)]
+    cu, new = _i32(np.concatenate([[0], np.cumsum(lens)])), torch.tensor(lens, dtype=torch.int32).pin_memory()
+
+    def run(stream):
+        tables = torch.full((N, 4), -1, dtype=torch.int32, device=DEV)
+        ring, ctx = torch.arange(16, dtype=torch.int32, device=DEV), torch.zeros(N, dtype=torch.int32, device=DEV)
+        state = _i32([0, 16])
+        caches = [torch.zeros(16, bs, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        d = [torch.zeros_like(x, device=DEV) for x in host]
+        n = torch.zeros(N, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(2_000_000)
+            for x, h in zip(d + [n], host + [new]):
+                x.copy_(h, non_blocking=True)
+            p = gdn.paged_plan(ctx, n, tables, ring, state, bs, T)
+            gdn.paged_write(d[1], d[1], p.slot_map, *caches)
+            out = gdn.recurrent_step(*d[:5], d[5], d[6], p.cu_seqlens, context_lens=ctx)
+        stream.synchronize()
+        assert torch.equal(p.cu_seqlens, cu)
+        return [*p, tables, ring, *caches, out, d[5]]
+
+    for a, b in zip(run(torch.cuda.current_stream()), run(torch.cuda.Stream())):
+        assert torch.equal(a, b)
