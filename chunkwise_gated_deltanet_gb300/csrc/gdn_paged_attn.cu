@@ -372,7 +372,6 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   k.s.T = a.T; k.s.g = a.Hq / a.Hkv; k.s.by_g = FastDiv((unsigned)k.s.g);
   k.s.by_hkv = FastDiv((unsigned)a.Hkv); k.s.Hkv = a.Hkv; k.s.window = a.window;
   k.s.max_blocks = a.max_blocks; k.s.max_kv = (long long)a.max_blocks * a.block_size;
-  k.s.min_tiles = 1;
   k.s.unit_cost = 1;
   k.part_o = reinterpret_cast<float*>(a.workspace);
   // Launches over ranges of requests, `most` at a time, and few enough that the costs of their

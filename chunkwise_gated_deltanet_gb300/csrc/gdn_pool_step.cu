@@ -11,9 +11,11 @@
 // dozen on (8 dk dv operations a token).  Two kernels, chosen by the tokens a request has on
 // average, T / N (bf16, heads of 128; us of the one / the other):
 //
-//   up to 14  token by token on the CUDA cores    1 to 8 tokens x 256 requests of 16 heads: 98 / 141;
-//                                                  12 x 128: 100 / 114; 16 x 128: 117 / 114
-//   above     8 at a time on the tensor cores     24 x 96: 133 / 118; 1 to 64 x 48 of 32 heads: 223 / 158
+//   up to 14  token by token on the CUDA cores    1 to 8 tokens x 256 requests of 16 heads: 98 / 138;
+//                                                  12 x 128: 97 / 102; 16 x 128: 115 / 102
+//   above     8 at a time on the tensor cores     24 x 96: 132 / 103; 1 to 64 x 48 of 32 heads: 220 / 135
+//
+// (1 to 8 x 256 moves 0.55 GB, which is 81 us at the measured copy rate.)
 //
 // Both stage k, q, v of 8 tokens by cp.async while the 8 before are computed, and read and
 // write a unit's state, one (request, head), once.
@@ -39,10 +41,11 @@
 //
 // The products with S0 and the update run on mma.sync (m16n8k8, TF32) in three passes of
 // two-part operands (hi hi + hi lo + lo hi, about 2^-23 relative, fp32 sums), two where k and q
-// are bf16, which TF32 holds exactly; the sums over s < t are eight steps in registers.  A warp has 16 rows of S in the accumulators' layout for
-// the whole call.  The same registers are the products' left operand: an accumulator's columns
-// 2 t and 2 t + 1 stand for the operand's t and t + 4, and the right operands are laid out in
-// shared memory in that order, a piece a lane (hi, and lo where there is one, of both values).
+// are bf16, which TF32 holds exactly; the sums over s < t are eight steps in registers.  A warp
+// has 16 rows of S in the accumulators' layout for the whole call.  The same registers are the
+// products' left operand: an accumulator's columns 2 t and 2 t + 1 stand for the operand's t and
+// t + 4, and the right operands are laid out in shared memory in that order, a piece a lane (hi,
+// and lo where there is one, of both values).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -49,7 +49,6 @@ struct SchedArgs {
   long long max_kv;           // max_blocks * block_size
   int rows_lo, rows_hi;       // requests with rows in (rows_lo, rows_hi] only
   int unit_cost;              // what a unit costs apart from its tiles, in tiles
-  int min_tiles;              // tiles a CTA takes at least (while there are that many)
   long long wave_tokens;      // WAVES: cached tokens (all heads) above which waves are used
 };
 
@@ -100,7 +99,7 @@ struct SchedMem {
 template <int M, int BN, int NMAX, bool WAVES>
 struct Sched {
   using Mem = SchedMem<NMAX, WAVES>;
-  static constexpr int kM = M, kTile = BN;
+  static constexpr int kM = M;
   SchedArgs s;
   const Mem* mem;
   int total, base, quot, first, pos, end, unit0;
@@ -183,7 +182,7 @@ struct Sched {
     }
     __syncthreads();
     total = carry;
-    G = min(grid, max((total + s.min_tiles - 1) / s.min_tiles, 1));
+    G = min(grid, max(total, 1));
     cta = cta_id;
     base = 0;
     waves = 0;

@@ -514,8 +514,11 @@ int gdn_paged_write(const void* k, const void* v, const int32_t* slot_map, void*
  *            on the work of one request, which has to stay below 2^31 tiles
  * scale      positive
  *
- * Scores, softmax and sums are fp32; out is rounded once.  Deterministic.  Asynchronous;
- * errors as gdn_paged_write, and GDN_EINVAL for a short workspace.
+ * Scores, softmax statistics and sums are fp32.  With bf16 the probabilities are rounded to
+ * bf16 for the product with the values (the sum they are divided by, and lse, take them as
+ * they were), and out is rounded once.  Deterministic.  Two launches, three for bf16 batches
+ * of both few and many rows a request.  Asynchronous; errors as gdn_paged_write, and
+ * GDN_EINVAL for a short workspace.
  */
 int gdn_paged_attention(const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* block_tables, const int32_t* seq_lens,
@@ -545,8 +548,10 @@ size_t gdn_paged_attention_workspace_bytes(int Hq, int Hkv, int d, int max_q_len
  *            whatever its slot holds; a new request without tokens leaves its slot as it is
  * out        [T, H, dv] qkv_dtype, written for every token of every request
  *
- * fp32 arithmetic on the CUDA cores, token by token: meant for a token to a few dozen per
- * request (longer prompts: gdn_chunk_fwd).  Asynchronous; errors as gdn_paged_write.
+ * fp32 state, sums and accuracy: token by token on the CUDA cores where the requests have
+ * up to 14 tokens on average (T / N), 8 tokens at a time on the tensor cores above, with
+ * operands in two TF32 parts.  A request's tokens are one serial chain a head: gdn_chunk_fwd is
+ * for long prompts of few requests.  Deterministic.  Asynchronous; errors as gdn_paged_write.
  */
 int gdn_recurrent_step(const void* q, const void* k, const void* v, const float* log_alpha,
                        const float* beta, float* state_pool, const int32_t* state_index,
