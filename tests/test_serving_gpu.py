@@ -593,3 +593,30 @@ def test_plan_write_and_step_on_another_stream(lens):
 
     for a, b in zip(run(torch.cuda.current_stream()), run(torch.cuda.Stream())):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ql,kv", [(3, 500), (7, 200), (8, 2000), (13, 700), (30, 700), (100, 800)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_attention_values_that_all_rows_see(ql, kv, bad, dtype):
+    """A non-finite value in a tile that every row sees whole: its column gets it, from 12 rows
+    to several row blocks; the other columns are as without it."""
+    def edit(n, k, v):
+        v[9, :, 7] = bad
+    o, z, (ro, rz, A, X) = _attend([ql], [kv], 4, 1, 128, 16, dtype, edit=edit, seed=ql)[0]
+    got = o[:, :, 7]
+    assert torch.isnan(got).all() if math.isnan(bad) else (got == bad).all()
+    cols = [c for c in range(128) if c != 7]
+    to, tz = R.bounds(ro, rz, A, X, 128, kv, dtype == "bf16")
+    assert ((o - ro).abs() <= to)[:, :, cols].all() and ((z - rz).abs() <= tz).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g,ql,kv,window", [(8, 4, 5000, 0), (8, 4, 130, 0), (4, 8, 8, 0), (8, 3, 100, 7),
+                                            (4, 16, 3001, 0), (8, 8, 128, 0), (8, 7, 1000, 200), (16, 2, 33, 0)])
+def test_attention_units_of_up_to_64_rows(g, ql, kv, window, d):
+    """Units that the tensor-core kernel holds in 2 or 4 copies, whole and split, with rows that
+    see nothing in some copies' columns."""
+    q_lens, kv_lens = [ql, ql, 1, ql - 1], [kv, max(ql - 2, 1), 60, kv // 2 + ql]
+    res = _attend(q_lens, kv_lens, 2 * g, 2, d, 16, "bf16", window=window, seed=g + ql)
+    _check_attend(res, d, kv_lens, True)
