@@ -670,8 +670,12 @@ int paged_tc_requests() { return kTcRequests; }
 
 cudaError_t launch_paged_tc(AttnArgs a, int d, int grid, cudaStream_t stream) {
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * grid * kTcM * d);
+  // A unit's start, its tile on the diagonal, its output and what the join has of it count as 5
+  // tiles.  Measured with 2 / 5 / 8: one request of 8192 tokens without context 468 / 391 / 400
+  // us, 8 of 2048 325 / 304 / 310, 8 tokens x 256 requests 162 / 155 / 158, 4 tokens over 131k
+  // 68 / 66 / 65; two of 2000 over 20k to 30k 946 with any.
+  a.s.unit_cost = 5;
   // whole units in waves when keys and values pass half of the L2 cache (129 MB)
-  a.s.unit_cost = 2;
   a.s.wave_tokens = (64LL << 20) / ((long long)a.s.Hkv * d * 4);
   return d == 128 ? launch_tc_d<128>(a, grid, stream) : launch_tc_d<64>(a, grid, stream);
 }
