@@ -364,6 +364,28 @@ bool paged_attn_fits(const PagedAttnArgs& a) {
   return request_cost(a, p.tc ? 256 : 16, p.tc ? 128 : 64, kAll) <= kMostCost;
 }
 
+// Units that all find a CTA at once are not cut where they have few tiles, by the host's bounds
+// on the lengths: no parts, no joins, and a launch less.  What cutting would save is the tiles
+// that idle CTAs could take, T (1 - units / CTAs) of a unit's T; up to `few` of them cost no
+// more than the join.  (T itself is at most twice that: requests may be much shorter than the
+// longest.)  Measured on the GPU, cut / whole, us:
+//   few rows       3 requests decoding (12 units) 256 tokens 8.1 / 7.2, 512 9.8 / 10.2, 1000
+//                  9.9 / 16.9 (and 3 us of the host's for the launch); 70 (280 units) up to 500
+//                  15.2 / 12.0, up to 1000 19.6 / 19.0
+//   tensor cores   2 x 100 tokens (4 units) over 0 21.3 / 16.2, 500 22.5 / 22.7, 2000 32.0 / 38.8;
+//                  8 x 10 to 64 (64 units) over up to 1500 36.1 / 30.1
+//   CUDA cores     2 x 200 to 320 tokens in fp32 (40 units), window 64 23.9 / 21.0, 128 21.8 / 26.5
+constexpr int kFewMma = 10, kFewTc = 8, kFewSimt = 3;
+
+bool keep_whole(const PagedAttnArgs& a, int M, int BN, int rows_hi, int ctas, int few) {
+  const long long room = (long long)a.max_blocks * a.block_size, g = a.Hq / a.Hkv;
+  long long seen = a.max_seq_len > 0 ? std::min<long long>(a.max_seq_len, room) : room;
+  if (a.window > 0) seen = std::min<long long>(seen, (long long)a.window + (M + g - 1) / g + BN);
+  const double units = double((std::min<long long>(a.max_q_len * g, rows_hi) + M - 1) / M) * a.Hkv * a.N;
+  const double tiles = double((seen + BN - 1) / BN);
+  return units <= ctas && tiles <= 2 * few && tiles * (1 - units / ctas) <= few;
+}
+
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
   const Plan p = plan_of(a.bf16, a.d, (long long)a.max_q_len * (a.Hq / a.Hkv));
@@ -380,7 +402,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   k.part_o = reinterpret_cast<float*>(a.workspace);
   // Launches over ranges of requests, `most` at a time, and few enough that the costs of their
   // units (M rows, BN tokens a tile, by the host's bounds on the lengths) stay below 2^31.
-  auto ranges = [&](int most, int M, int BN, int rows_lo, int rows_hi, auto launch) {
+  auto ranges = [&](int most, int M, int BN, int rows_lo, int rows_hi, int ctas, int few, auto launch) {
+    k.s.whole = keep_whole(a, M, BN, rows_hi, ctas, few);
     k.s.rows_lo = rows_lo;
     k.s.rows_hi = rows_hi;
     most = (int)std::max(1.0, std::min<double>(most, kMostCost / request_cost(a, M, BN, rows_hi)));
@@ -398,18 +421,18 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (p.simt) {
     k.part_ml = reinterpret_cast<float2*>(k.part_o + (size_t)2 * grid * p.simt * a.d);
-    return ranges(kSimtRequests, p.simt, kBN, 0, kAll, [&] {
+    return ranges(kSimtRequests, p.simt, kBN, 0, kAll, grid, kFewSimt, [&] {
       return p.simt == 16 ? launch_simt_d<16>(k, a.d, a.bf16, grid, stream)
                           : launch_simt_d<64>(k, a.d, a.bf16, grid, stream);
     });
   }
   if (p.tc) {
     // a single request is taken whatever its length, so that nothing is left over
-    e = ranges(paged_tc_requests(), 256, 128, a.N > 1 ? 16 : 0, kAll,
+    e = ranges(paged_tc_requests(), 256, 128, a.N > 1 ? 16 : 0, kAll, grid, kFewTc,
                [&] { return launch_paged_tc(k, a.d, grid, stream); });
     if (e != cudaSuccess || a.N == 1) return e;
   }
-  return ranges(paged_mma_requests(), 16, 64, 0, p.tc ? 16 : kAll,
+  return ranges(paged_mma_requests(), 16, 64, 0, p.tc ? 16 : kAll, 2 * sm_count(), kFewMma,
                 [&] { return launch_paged_mma(k, a.d, stream); });
 }
 

@@ -80,7 +80,7 @@ __device__ __forceinline__ void st4f(void* p, size_t i, float4 x) {
   }
 }
 
-// x = hi + lo with hi rounded to TF32's 11 significant bits; lo is cut to them by the product.
+// x = hi + lo with hi rounded to TF32's 11 significant bits and lo cut to them.
 __device__ __forceinline__ uint32_t tf_hi(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ uint32_t tf_lo(float x, uint32_t hi) {
   return __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 // (its inputs are older than that kernel).
 template <int D, typename SCHED>
 cudaError_t launch_join(const AttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
-  if (grid < 2) return cudaSuccess;
+  if (grid < 2 || a.s.whole) return cudaSuccess;
   const dim3 ctas(grid - 1, std::max(1, SCHED::kM / 64));
   return bf16 ? launch_early(paged_join_kernel<D, SCHED, true>, ctas, kJoinThreads, 0, stream, a, grid)
               : launch_early(paged_join_kernel<D, SCHED, false>, ctas, kJoinThreads, 0, stream, a, grid);

@@ -49,6 +49,7 @@ struct SchedArgs {
   long long max_kv;           // max_blocks * block_size
   int rows_lo, rows_hi;       // requests with rows in (rows_lo, rows_hi] only
   int unit_cost;              // what a unit costs apart from its tiles, in tiles
+  int whole;                  // units are not cut: shares are whole units, whatever they cost
   long long wave_tokens;      // WAVES: cached tokens (all heads) above which waves are used
 };
 
@@ -122,7 +123,7 @@ struct Sched {
   __device__ __forceinline__ int cost(const Req& q, int b) const {
     int l;
     bool e;
-    return tiles(q, b, &l, &e) + s.unit_cost;
+    return s.whole ? 1 : tiles(q, b, &l, &e) + s.unit_cost;
   }
   __device__ __forceinline__ static int blocks(const Req& q) { return (q.rows + M - 1) / M; }
 
@@ -194,7 +195,7 @@ struct Sched {
       __syncthreads();
       tokens = 0.f;
       for (int w = 0; w < NT / 32; ++w) tokens += __int_as_float(m->warp[w]);
-      if (tokens > s.wave_tokens) waves = max(carry_u / G - 1, 0);
+      if (tokens > s.wave_tokens && !s.whole) waves = max(carry_u / G - 1, 0);
       if (waves > 0) {
         find_unit(waves * G);
         base = unit0;
@@ -327,6 +328,14 @@ struct Sched {
       return true;
     }
     if (pos >= end) return false;
+    if (s.whole) {
+      locate(pos++);
+      int lo;
+      bool empty;
+      const int c = tiles(r, blk, &lo, &empty);
+      *it = Item{n, h, blk, r, empty ? 0 : lo, empty ? 0 : lo + c, true, 0};
+      return true;
+    }
     if (!started) {
       locate(pos);
       started = true;

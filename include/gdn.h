@@ -516,8 +516,9 @@ int gdn_paged_write(const void* k, const void* v, const int32_t* slot_map, void*
  *
  * Scores, softmax statistics and sums are fp32.  With bf16 the probabilities are rounded to
  * bf16 for the product with the values (the sum they are divided by, and lse, take them as
- * they were), and out is rounded once.  Deterministic.  Two launches, three for bf16 batches
- * of both few and many rows a request.  Asynchronous; errors as gdn_paged_write, and
+ * they were), and out is rounded once.  Deterministic.  One launch, or two
+ * where requests are split over CTAs; twice that for bf16 batches of both few and many rows
+ * a request.  Asynchronous; errors as gdn_paged_write, and
  * GDN_EINVAL for a short workspace.
  */
 int gdn_paged_attention(const void* q, const void* k_cache, const void* v_cache,

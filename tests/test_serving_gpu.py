@@ -620,3 +620,48 @@ def test_attention_units_of_up_to_64_rows(g, ql, kv, window, d):
     q_lens, kv_lens = [ql, ql, 1, ql - 1], [kv, max(ql - 2, 1), 60, kv // 2 + ql]
     res = _attend(q_lens, kv_lens, 2 * g, 2, d, 16, "bf16", window=window, seed=g + ql)
     _check_attend(res, d, kv_lens, True)
+
+
+@pytest.mark.parametrize("dtype,max_q,q_lens", [("bf16", 1, [12, 1, 40]), ("bf16", 5, [200, 3, 64]), ("f32", 2, [90, 1, 33])])
+def test_attention_more_units_than_the_host_expects(dtype, max_q, q_lens):
+    """max_q_len and max_seq_len below the truth: the units that the host does not expect are
+    done all the same, several a CTA."""
+    N, Hq, Hkv, d, block = 36, 16, 4, 64, 16
+    ql = [q_lens[n % 3] for n in range(N)]
+    kv = [ql[n] + 11 * (n % 5) for n in range(N)]
+    kc, vc, tables, keys, values = R.pages(kv, Hkv, d, block, DT[dtype], 5, DEV)
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(sum(ql), Hq, d, generator=g).to(DT[dtype]).to(DEV)
+    cu = np.concatenate([[0], np.cumsum(ql)])
+    out, lse = gdn.paged_attention(q, kc, vc, tables, _i32(kv), _i32(cu), max_q, max_seq_len=100, return_lse=True)
+    gdn.gdn_check_status()
+    res = []
+    for n in range(N):
+        sl = slice(cu[n], cu[n + 1])
+        ref = R.attention(q[sl], keys[n], values[n], kv[n] - ql[n], d ** -0.5, 0)
+        res.append((out[sl].double().cpu(), lse[sl].double().cpu(), ref))
+    _check_attend(res, d, kv, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ql", [1, 24])
+def test_attention_cut_and_whole_agree(ql, dtype):
+    """The same requests with the sequences' bound given (units stay whole) and with a table of
+    much more room (units are cut)."""
+    N, Hq, Hkv, d, block = 5, 8, 2, 128, 16
+    kv = [ql + x for x in (0, 37, 64, 90, 100)]
+    kc, vc, tables, keys, values = R.pages(kv, Hkv, d, block, DT[dtype], 7, DEV)
+    wide = torch.full((N, 4096), -1, dtype=torch.int32, device=DEV)
+    wide[:, :tables.shape[1]] = tables
+    g = torch.Generator().manual_seed(8)
+    q = torch.randn(N * ql, Hq, d, generator=g).to(DT[dtype]).to(DEV)
+    cu = _i32([n * ql for n in range(N + 1)])
+    for table, bound in ((tables, 128), (wide, 0)):
+        out, lse = gdn.paged_attention(q, kc, vc, table, _i32(kv), cu, ql, max_seq_len=bound, return_lse=True)
+        gdn.gdn_check_status()
+        res = []
+        for n in range(N):
+            sl = slice(n * ql, (n + 1) * ql)
+            ref = R.attention(q[sl], keys[n], values[n], kv[n] - ql, d ** -0.5, 0)
+            res.append((out[sl].double().cpu(), lse[sl].double().cpu(), ref))
+        _check_attend(res, d, kv, dtype == "bf16")
