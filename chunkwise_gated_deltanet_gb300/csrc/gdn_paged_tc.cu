@@ -31,10 +31,11 @@
 // rounded to bf16 for the tensor cores; l sums the unrounded values.
 //
 // Measured: 2 requests of about 2000 new tokens over 20,000 to 30,000 cached ones, 32 heads on
-// 8 of 128: 0.95 to 1.01 ms, 1.55 to 1.65 PFLOP/s of the 1.73 (sustained) to 1.96 (burst) of a
-// large product; the tensor pipe is busy 75 % of the time.  4 tokens over 131,075 (32 heads on
-// 4, one request): 67 us where the bytes take 40; four times the cache costs 38 us more a
-// 268 MB, so about 30 us are the start, the join and what surrounds the launches.
+// 8 of 128: 0.95 to 1.03 ms, 1.53 to 1.66 PFLOP/s of the 1.73 (sustained) to 1.96 (burst) of a
+// large product; the tensor pipe is busy 75 % of the time.  One request of 8192 tokens without
+// context: 0.39 ms.  4 tokens over 131,075 (32 heads on 4, one request): 66 us where the bytes
+// take 40; four times the cache costs 38 us more a 268 MB, so nearly 30 us are the start, the
+// join and what surrounds the launches.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
