@@ -3,23 +3,27 @@
 Each translation unit under ``csrc/`` compiles in parallel to ``_build/*.o``; the
 objects link into ``chunkwise_gated_deltanet_gb300/libgdn.so`` (static CUDA
 runtime, no torch).  Rebuilds only when a source or header is newer than its
-object.
+object.  ``csrc/serving_calls.cpp``, the serving operators' calls from Python, compiles with
+g++ against the installed PyTorch to ``_serving.so`` beside it, and again for another one.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build", platform.machine())
 LIB = os.path.join(PKG, "libgdn.so")
+CALLS = os.path.join(PKG, "_serving.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I" + os.path.join(ROOT, "include")]
@@ -44,6 +48,35 @@ def _stale(src: str, obj: str, newest_header: float) -> bool:
     return os.path.getmtime(src) > t or newest_header > t
 
 
+def build_calls(force: bool = False) -> str:
+    """``_serving.so``: rebuilt for a newer source or header, another PyTorch, Python or machine."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("PyTorch not found")
+    torch_dir = os.path.dirname(spec.origin)
+    src = os.path.join(CSRC, "serving_calls.cpp")
+    header = os.path.join(ROOT, "include", "gdn.h")
+    version = open(os.path.join(torch_dir, "version.py")).read()
+    key = "\n".join([platform.machine(), sys.version, torch_dir, version])
+    stamp = os.path.join(BUILD, "calls.stamp")
+    if not force and os.path.exists(CALLS) and os.path.exists(stamp) and open(stamp).read() == key and \
+            max(os.path.getmtime(src), os.path.getmtime(header)) <= os.path.getmtime(CALLS):
+        return CALLS
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *("-isystem" + i for i in include), src, "-o", tmp,
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed: " + " ".join(cmd))
+    os.replace(tmp, CALLS)
+    open(stamp, "w").write(key)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -55,6 +88,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         objs.append(o)
         if force or _stale(s, o, hdr_t):
             jobs.append([nvcc(), *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
+    calls = cf.ThreadPoolExecutor(max_workers=1).submit(build_calls, force)  # beside the kernels
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -73,6 +107,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError("nvcc link failed")
         os.replace(tmp, LIB)
         open(stamp, "w").write(platform.machine())
+    calls.result()
     return LIB
 
 

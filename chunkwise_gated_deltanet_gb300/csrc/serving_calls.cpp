@@ -1,0 +1,360 @@
+// The serving operators' calls from Python: argument checks, output tensors, and the calls of
+// the C entry points.  Nothing is computed here.
+//
+// A small step is as long as its host side: the kernels of a few requests take 3 to 10 us, and
+// after a launch each operation that the interpreter makes on a tensor takes 2 to 5 us.  Checked
+// and allocated in Python and called through ctypes, the calls of a few requests took 24 us
+// (paged_plan), 8.5 (paged_write), 25 (paged_attention) and 17 (recurrent_step), one after the
+// other; from here 7.7, 2.9, 10.4 (the GPU's time) and 4.6.
+#include <Python.h>
+
+#include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
+
+#include <array>
+#include <climits>
+#include <cmath>
+#include <string>
+
+#include "gdn.h"
+
+namespace {
+
+using at::Tensor;
+
+// The library's functions, as the package loaded them, and the exception of a refused call.
+struct Lib {
+  decltype(&gdn_paged_plan) plan;
+  decltype(&gdn_paged_write) write;
+  decltype(&gdn_paged_attention) attention;
+  decltype(&gdn_paged_attention_workspace_bytes) workspace_bytes;
+  decltype(&gdn_recurrent_step) step;
+  decltype(&gdn_last_error) last_error;
+  PyObject* error = nullptr;
+} lib;
+
+std::string describe(const Tensor& t) {
+  return c10::str(t.scalar_type(), " ", t.sizes(), " on ", t.device());
+}
+
+const Tensor& tensor(const char* fn, const char* name, PyObject* o) {
+  TORCH_CHECK_VALUE(THPVariable_Check(o), fn, ": ", name, " must be a CUDA tensor, got ", Py_TYPE(o)->tp_name);
+  return THPVariable_Unpack(o);
+}
+
+int device_of(const char* fn, const char* name, const Tensor& t) {
+  TORCH_CHECK_VALUE(t.is_cuda(), fn, ": ", name, " must be a CUDA tensor, got ", describe(t));
+  return (int)t.get_device();
+}
+
+int dtype_code(const Tensor& t) {
+  const auto dt = t.scalar_type();
+  TORCH_CHECK_TYPE(dt == at::kFloat || dt == at::kBFloat16, "q/k/v must be float32 or bfloat16, got ", dt);
+  return dt == at::kFloat ? GDN_F32 : GDN_BF16;
+}
+
+// A contiguous tensor of this type, shape and device; its address.
+void* need(const char* fn, const char* name, const Tensor& t, at::ScalarType dt, at::IntArrayRef shape, int dev) {
+  TORCH_CHECK_VALUE(t.scalar_type() == dt && t.sizes() == shape && t.is_cuda() && t.get_device() == dev &&
+                        t.is_contiguous(),
+                    fn, ": ", name, " must be a contiguous ", dt, " tensor of shape ", shape, " on cuda:", dev,
+                    ", got ", describe(t));
+  return t.data_ptr();
+}
+void* need(const char* fn, const char* name, PyObject* o, at::ScalarType dt, at::IntArrayRef shape, int dev) {
+  return need(fn, name, tensor(fn, name, o), dt, shape, dev);
+}
+int32_t* ints(const char* fn, const char* name, PyObject* o, at::IntArrayRef shape, int dev) {
+  return static_cast<int32_t*>(need(fn, name, o, at::kInt, shape, dev));
+}
+
+// [T, heads, d] with dense heads and any token stride; the token stride in elements.
+long long rows(const char* fn, const char* name, const Tensor& t, at::ScalarType dt, int dev) {
+  TORCH_CHECK_VALUE(t.scalar_type() == dt && t.dim() == 3 && t.is_cuda() && t.get_device() == dev, fn, ": ", name,
+                    " must be a ", dt, " tensor [T, heads, d] on cuda:", dev, ", got ", describe(t));
+  const auto n = t.sizes(), s = t.strides();
+  TORCH_CHECK_VALUE((s[2] == 1 || n[2] <= 1) && (s[1] == n[2] || n[1] <= 1), fn, ": ", name,
+                    " must be [T, heads, d] with dense heads, got ", describe(t));
+  return n[0] > 1 ? s[0] : n[1] * n[2];
+}
+
+int size(const char* fn, const char* name, long long x) {
+  TORCH_CHECK_VALUE(x >= INT_MIN && x <= INT_MAX, fn, ": ", name, " must be below 2^31, got ", x);
+  return (int)x;
+}
+int number(const char* fn, const char* name, PyObject* o) {
+  const long long x = PyLong_AsLongLong(o);
+  if (x == -1 && PyErr_Occurred()) throw python_error();
+  return size(fn, name, x);
+}
+
+void* stream_of(PyObject* o, int dev) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+  void* s = PyLong_AsVoidPtr(o);
+  if (!s && PyErr_Occurred()) throw python_error();
+  return s;
+}
+
+template <typename F>
+void call(F f) {
+  int status;
+  Py_BEGIN_ALLOW_THREADS;
+  status = f();
+  Py_END_ALLOW_THREADS;
+  if (status == GDN_OK) return;
+  PyObject* e = PyObject_CallFunction(lib.error, "is", status, lib.last_error());
+  if (e) {
+    PyErr_SetObject(lib.error, e);
+    Py_DECREF(e);
+  }
+  throw python_error();
+}
+
+void arguments(const char* fn, Py_ssize_t got, Py_ssize_t want) {
+  TORCH_CHECK_TYPE(got == want, fn, " takes ", want, " arguments, got ", got);
+}
+
+// bind(plan, write, attention, workspace_bytes, step, last_error, error): addresses, class
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("bind", n, 7);
+  void* p[6];
+  for (int i = 0; i < 6; ++i)
+    if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
+      if (PyErr_Occurred()) throw python_error();
+      TORCH_CHECK_VALUE(false, "bind: a null address");
+    }
+  lib.plan = reinterpret_cast<decltype(lib.plan)>(p[0]);
+  lib.write = reinterpret_cast<decltype(lib.write)>(p[1]);
+  lib.attention = reinterpret_cast<decltype(lib.attention)>(p[2]);
+  lib.workspace_bytes = reinterpret_cast<decltype(lib.workspace_bytes)>(p[3]);
+  lib.step = reinterpret_cast<decltype(lib.step)>(p[4]);
+  lib.last_error = reinterpret_cast<decltype(lib.last_error)>(p[5]);
+  Py_INCREF(a[6]);
+  Py_XSETREF(lib.error, a[6]);
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// plan(context_lens, new_lens, block_tables, free_ring, ring_in, outputs, T, block_size, stream):
+// outputs None (made here and returned, in PagedPlan's order) or a tuple in that order.
+PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  const bool make = nargs > 5 && a[5] == Py_None;
+  const char* fn = make ? "paged_plan" : "gdn_paged_plan";
+  arguments(fn, nargs, 9);
+  const Tensor &ctx = tensor(fn, "context_lens", a[0]), &bt = tensor(fn, "block_tables", a[2]);
+  const int dev = device_of(fn, "context_lens", ctx);
+  const int N = size(fn, "context_lens", ctx.numel());
+  const int nb = size(fn, "free_ring", tensor(fn, "free_ring", a[3]).numel());
+  TORCH_CHECK_VALUE(bt.dim() == 2, fn, ": block_tables must be [N, max_blocks], got ", describe(bt));
+  const int M = size(fn, "block_tables", bt.size(1)), bs = number(fn, "block_size", a[7]);
+  const int32_t* cl = static_cast<int32_t*>(need(fn, "context_lens", ctx, at::kInt, {N}, dev));
+  const int32_t* nl = ints(fn, "new_lens", a[1], {N}, dev);
+  int32_t* tables = static_cast<int32_t*>(need(fn, "block_tables", bt, at::kInt, {N, M}, dev));
+  int32_t* ring = ints(fn, "free_ring", a[3], {nb}, dev);
+  const int32_t* ring_in = ints(fn, "ring_in", a[4], {2}, dev);
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+  int T;
+  int32_t* out[6];
+  Tensor buffer;
+  int64_t sizes[6];
+  if (make) {
+    T = number(fn, "num_tokens", a[6]);
+    TORCH_CHECK_VALUE(T >= 0, fn, ": num_tokens must be >= 0, got ", T);
+    const at::AutoDispatchBelowADInplaceOrView below;
+    const int64_t want[6] = {N + 1ll, N, T, T, N, 2};
+    int64_t all = 0;
+    for (int i = 0; i < 6; ++i) all += sizes[i] = want[i];
+    buffer = at::empty({all}, ctx.options());  // one allocation for the six outputs
+    int32_t* p = static_cast<int32_t*>(buffer.data_ptr());
+    for (int i = 0; i < 6; p += sizes[i++]) out[i] = sizes[i] ? p : nullptr;
+  } else {
+    TORCH_CHECK_TYPE(PyTuple_Check(a[5]) && PyTuple_GET_SIZE(a[5]) == 6, fn, ": six outputs");
+    auto item = [&](int i) { return PyTuple_GET_ITEM(a[5], i); };
+    T = size(fn, "slot_map", tensor(fn, "slot_map", item(2)).numel());
+    out[0] = ints(fn, "cu_seqlens", item(0), {N + 1ll}, dev);
+    out[1] = ints(fn, "seq_lens", item(1), {N}, dev);
+    out[2] = ints(fn, "slot_map", item(2), {T}, dev);
+    out[3] = ints(fn, "positions", item(3), {T}, dev);
+    out[4] = ints(fn, "granted", item(4), {N}, dev);
+    out[5] = ints(fn, "ring_out", item(5), {2}, dev);
+  }
+  void* stream = stream_of(a[8], dev);
+  call([&] {
+    return lib.plan(cl, nl, tables, ring, ring_in, out[5], out[0], out[1], out[2], out[3], out[4], N, T, M, nb, bs,
+                    stream);
+  });
+  if (!make) Py_RETURN_NONE;
+  THPObjectPtr result(PyTuple_New(6));
+  if (!result) throw python_error();
+  const at::AutoDispatchBelowADInplaceOrView below;
+  int64_t at_ = 0;
+  for (int i = 0; i < 6; at_ += sizes[i++]) {
+    PyObject* x = THPVariable_Wrap(buffer.as_strided({sizes[i]}, {1}, at_));
+    if (!x) throw python_error();
+    PyTuple_SET_ITEM(result.get(), i, x);
+  }
+  return result.release();
+  END_HANDLE_TH_ERRORS
+}
+
+// write(k, v, slot_map, k_cache, v_cache, stream)
+PyObject* write(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  const char* fn = "gdn_paged_write";
+  arguments(fn, nargs, 6);
+  const Tensor &k = tensor(fn, "k", a[0]), &v = tensor(fn, "v", a[1]), &kc = tensor(fn, "k_cache", a[3]);
+  const int code = dtype_code(kc), dev = device_of(fn, "k_cache", kc);
+  const auto dt = kc.scalar_type();
+  const auto n = kc.sizes();
+  TORCH_CHECK_VALUE(n.size() == 4, fn, ": k_cache must be [num_blocks, block_size, Hkv, d], got ", describe(kc));
+  const long long ks = rows(fn, "k", k, dt, dev), vs = rows(fn, "v", v, dt, dev);
+  const int64_t T = k.size(0);
+  const std::array<int64_t, 3> row{T, n[2], n[3]};
+  TORCH_CHECK_VALUE(k.sizes() == at::IntArrayRef(row) && v.sizes() == at::IntArrayRef(row), fn,
+                    ": k and v must be [T, ", n[2], ", ", n[3], "], got ", k.sizes(), " and ", v.sizes());
+  const int32_t* slots = ints(fn, "slot_map", a[2], {T}, dev);
+  void* kp = need(fn, "k_cache", kc, dt, n, dev);
+  void* vp = need(fn, "v_cache", a[4], dt, n, dev);
+  const int Ti = size(fn, "T", T), H = size(fn, "Hkv", n[2]), d = size(fn, "d", n[3]);
+  const int nb = size(fn, "num_blocks", n[0]), bs = size(fn, "block_size", n[1]);
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+  const void *kin = k.data_ptr(), *vin = v.data_ptr();
+  void* stream = stream_of(a[5], dev);
+  call([&] { return lib.write(kin, vin, slots, kp, vp, Ti, H, d, nb, bs, ks, vs, code, stream); });
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// attention(q, k_cache, v_cache, block_tables, seq_lens, cu_seqlens, out, lse, workspace, max_q_len,
+//           max_seq_len, scale, window, stream)
+// out None: made here, with lse where that is True, and a workspace where that is None;
+// returned are out, or (out, lse).
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  const bool make = nargs > 6 && a[6] == Py_None;
+  const char* fn = make ? "paged_attention" : "gdn_paged_attention";
+  arguments(fn, nargs, 14);
+  const Tensor &q = tensor(fn, "q", a[0]), &kc = tensor(fn, "k_cache", a[1]), &bt = tensor(fn, "block_tables", a[3]);
+  const int dev = device_of(fn, "q", q), code = dtype_code(q);
+  const auto dt = q.scalar_type();
+  const long long qs = rows(fn, "q", q, dt, dev);
+  const auto n = kc.sizes();
+  TORCH_CHECK_VALUE(n.size() == 4 && n[3] == q.size(2) && bt.dim() == 2, fn,
+                    ": k_cache must be [num_blocks, block_size, Hkv, ", q.size(2),
+                    "] and block_tables [N, max_blocks], got ", n, " and ", bt.sizes());
+  const int T = size(fn, "T", q.size(0)), Hq = size(fn, "Hq", q.size(1)), d = size(fn, "d", q.size(2));
+  const int nb = size(fn, "num_blocks", n[0]), bs = size(fn, "block_size", n[1]), Hkv = size(fn, "Hkv", n[2]);
+  const int N = size(fn, "N", bt.size(0)), M = size(fn, "max_blocks", bt.size(1));
+  const int mq = number(fn, "max_q_len", a[9]), ms = number(fn, "max_seq_len", a[10]);
+  const int window = number(fn, "window", a[12]);
+  double scale = 0;
+  if (a[11] == Py_None) {
+    scale = 1 / std::sqrt((double)d);
+  } else {
+    scale = PyFloat_AsDouble(a[11]);
+    if (scale == -1 && PyErr_Occurred()) throw python_error();
+  }
+  void* kp = need(fn, "k_cache", kc, dt, n, dev);
+  void* vp = need(fn, "v_cache", a[2], dt, n, dev);
+  const int32_t* tables = static_cast<int32_t*>(need(fn, "block_tables", bt, at::kInt, {N, M}, dev));
+  const int32_t* sl = ints(fn, "seq_lens", a[4], {N}, dev);
+  const int32_t* cu = ints(fn, "cu_seqlens", a[5], {N + 1ll}, dev);
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+  Tensor out, lse, ws;
+  {
+    const at::AutoDispatchBelowADInplaceOrView below;
+    if (make) {
+      out = at::empty(q.sizes(), q.options());
+      if (a[7] == Py_True) lse = at::empty({T, Hq}, q.options().dtype(at::kFloat));
+    } else {
+      out = tensor(fn, "out", a[6]);
+      need(fn, "out", out, dt, q.sizes(), dev);
+      if (a[7] != Py_None) {
+        lse = tensor(fn, "lse", a[7]);
+        need(fn, "lse", lse, at::kFloat, {T, Hq}, dev);
+      }
+    }
+    if (make && a[8] == Py_None) {
+      const int64_t bytes = (int64_t)lib.workspace_bytes(Hq, Hkv, d, mq, code);
+      ws = at::empty({bytes > 0 ? bytes : 1}, q.options().dtype(at::kByte));
+    } else {
+      ws = tensor(fn, "workspace", a[8]);
+      TORCH_CHECK_VALUE(ws.is_cuda() && ws.get_device() == dev && ws.is_contiguous(), fn,
+                        ": workspace must be a contiguous tensor on cuda:", dev, ", got ", describe(ws));
+    }
+  }
+  const void* qp = q.data_ptr();
+  void *op = out.data_ptr(), *wp = ws.data_ptr(), *stream = stream_of(a[13], dev);
+  float* lp = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
+  const size_t bytes = ws.nbytes();
+  call([&] {
+    return lib.attention(qp, kp, vp, tables, sl, cu, op, lp, wp, bytes, N, T, Hq, Hkv, d, M, nb, bs, mq, ms, window,
+                         (float)scale, qs, code, stream);
+  });
+  if (!make) Py_RETURN_NONE;
+  if (!lse.defined()) return THPVariable_Wrap(out);
+  THPObjectPtr o(THPVariable_Wrap(out)), l(THPVariable_Wrap(lse));
+  if (!o || !l) throw python_error();
+  return PyTuple_Pack(2, o.get(), l.get());
+  END_HANDLE_TH_ERRORS
+}
+
+// step(q, k, v, log_alpha, beta, state_pool, state_index, cu_seqlens, out, context_lens, stream):
+// out None: made here and returned.
+PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  const bool make = nargs > 8 && a[8] == Py_None;
+  const char* fn = make ? "recurrent_step" : "gdn_recurrent_step";
+  arguments(fn, nargs, 11);
+  const Tensor &q = tensor(fn, "q", a[0]), &k = tensor(fn, "k", a[1]), &v = tensor(fn, "v", a[2]);
+  const Tensor &pool = tensor(fn, "state_pool", a[5]), &index = tensor(fn, "state_index", a[6]);
+  const int dev = device_of(fn, "v", v), code = dtype_code(v);
+  const auto dt = v.scalar_type();
+  const long long qs = rows(fn, "q", q, dt, dev), ks = rows(fn, "k", k, dt, dev), vs = rows(fn, "v", v, dt, dev);
+  TORCH_CHECK_VALUE(q.sizes() == k.sizes() && v.size(0) == k.size(0) && pool.dim() == 4, fn,
+                    ": need q, k [T, Hk, dk], v [T, H, dv] and state_pool [slots, H, dv, dk], got ", q.sizes(), ", ",
+                    k.sizes(), ", ", v.sizes(), ", ", pool.sizes());
+  const int T = size(fn, "T", k.size(0)), Hk = size(fn, "Hk", k.size(1)), dk = size(fn, "dk", k.size(2));
+  const int H = size(fn, "H", v.size(1)), dv = size(fn, "dv", v.size(2));
+  const int N = size(fn, "N", index.numel()), slots = size(fn, "slots", pool.size(0));
+  const float* la = static_cast<float*>(need(fn, "log_alpha", a[3], at::kFloat, {T, H}, dev));
+  const float* be = static_cast<float*>(need(fn, "beta", a[4], at::kFloat, {T, H}, dev));
+  float* sp = static_cast<float*>(need(fn, "state_pool", pool, at::kFloat, {slots, H, dv, dk}, dev));
+  const int32_t* si = static_cast<int32_t*>(need(fn, "state_index", index, at::kInt, {N}, dev));
+  const int32_t* cu = ints(fn, "cu_seqlens", a[7], {N + 1ll}, dev);
+  const int32_t* cl = a[9] == Py_None ? nullptr : ints(fn, "context_lens", a[9], {N}, dev);
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+  Tensor out;
+  if (make) {
+    const at::AutoDispatchBelowADInplaceOrView below;
+    out = at::empty(v.sizes(), v.options());
+  } else {
+    out = tensor(fn, "out", a[8]);
+    need(fn, "out", out, dt, v.sizes(), dev);
+  }
+  const void *qp = q.data_ptr(), *kp = k.data_ptr(), *vp = v.data_ptr();
+  void *op = out.data_ptr(), *stream = stream_of(a[10], dev);
+  call([&] {
+    return lib.step(qp, kp, vp, la, be, sp, si, cu, cl, op, N, T, Hk, H, dk, dv, slots, qs, ks, vs, code, stream);
+  });
+  if (!make) Py_RETURN_NONE;
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+#define GDN_CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {GDN_CALL(bind),      GDN_CALL(plan), GDN_CALL(write),
+                         GDN_CALL(attention), GDN_CALL(step), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__serving() { return PyModule_Create(&module_def); }

