@@ -3,7 +3,10 @@
 // cache (gdn_paged_write).
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "early_launch.cuh"
+#include "fast_div.cuh"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -18,12 +21,14 @@ namespace {
 // Bound by launch and memory latency: about 1 MB moves for 4096 requests and 65,000
 // tokens.  So it is one launch with no communication between CTAs: every CTA scans all
 // requests itself (two loads a request, 2048 requests a round) and takes a stripe of
-// the tokens, table entries and released blocks, finding an item's request by binary
+// the list of tokens, table entries and released blocks, finding an item's request by binary
 // search in the round's prefix sums in shared memory.  In-place updates cannot race: the
 // entries that a call writes (table entries from old_n on, ring positions past the free
 // range) are none of those it reads.
 //
-// Measured: 8 requests 4.5 us, 4096 requests with 65,000 new tokens 16 us.
+// Measured: 8 requests 3.5 us, 4096 requests with 65,000 new tokens 11.7 us.  With 2 or 8 requests
+// a thread 3.0 and 18.3, or 4.4 and 11.9; with tokens, entries and blocks one after the other and
+// 64-bit quotients 4.6 and 15.9.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanPer = 4;                          // requests a thread holds
 constexpr int kPlanChunk = kPlanThreads * kPlanPer;  // requests a round
@@ -57,49 +62,49 @@ __device__ __forceinline__ int sat32(long long x) {
   return x > 0x7fffffffLL ? 0x7fffffff : (int)x;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanArgs a) {
-  __shared__ int tok0[kPlanChunk + 1], need0[kPlanChunk + 1], back0[kPlanChunk + 1];
-  __shared__ unsigned char ok[kPlanChunk];
-  __shared__ Sum3 wsum[kPlanThreads / 32];
-  __shared__ int taken_s;
+// Of the requests of a round: where their tokens, needed and released blocks begin, and grants.
+struct PlanSmem {
+  int tok0[kPlanChunk + 1], need0[kPlanChunk + 1], back0[kPlanChunk + 1];
+  unsigned char ok[kPlanChunk];
+  Sum3 wsum[kPlanThreads / 32];
+  int taken;
+};
+
+__global__ void __launch_bounds__(kPlanThreads)
+paged_plan_kernel(const __grid_constant__ PlanArgs a, const __grid_constant__ FastDiv by_bs) {
+  __shared__ PlanSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_kernel_start();
   after_previous_kernel();
-  const long long cap = (long long)a.max_blocks * a.block_size;
-  const int bs = a.block_size, nb = a.num_blocks;
+  const int bs = a.block_size, nb = a.num_blocks, cap = a.max_blocks * bs;  // below 2^31 - 1024
   int head = a.ring_in[0] % nb;
   if (head < 0) head += nb;
   const int count = min(max(a.ring_in[1], 0), nb);
   const int stride = gridDim.x * kPlanThreads;
   const int me = blockIdx.x * kPlanThreads + tid;
-  if (tid == 0) taken_s = 0;
+  if (tid == 0) sm.taken = 0;
   Sum3 carry{0, 0, 0};
+  auto blocks = [&](int tokens) { return by_bs.div(min(tokens, cap) + bs - 1); };
+  auto ring = [&](int x) { return a.free_ring[x >= nb ? x - nb : x]; };  // x < 2 nb
 
   for (int n0 = 0, round = 0; n0 < a.N; n0 += kPlanChunk, ++round) {
     const int nn = min(kPlanChunk, a.N - n0);
     const bool writer = round % gridDim.x == blockIdx.x;
-    Sum3 mine[kPlanPer], sum{0, 0, 0};
-    int ctx[kPlanPer], add[kPlanPer];
-    bool fits[kPlanPer], done[kPlanPer];
+    int ctx[kPlanPer], nw[kPlanPer];
+    Sum3 sum{0, 0, 0};
 #pragma unroll
     for (int u = 0; u < kPlanPer; ++u) {
       const int n = n0 + tid * kPlanPer + u;
-      const bool in = n < a.N;
-      ctx[u] = in ? max(__ldg(a.context_lens + n), 0) : 0;
-      const int nw = in ? __ldg(a.new_lens + n) : 0;
-      done[u] = nw < 0;
-      add[u] = max(nw, 0);
+      ctx[u] = n < a.N ? max(__ldg(a.context_lens + n), 0) : 0;
+      nw[u] = n < a.N ? __ldg(a.new_lens + n) : 0;
     }
+    auto fits = [&](int u) { return nw[u] >= 0 && (long long)ctx[u] + nw[u] <= cap; };
+    auto part = [&](int u) {
+      const int old = blocks(ctx[u]);
+      return Sum3{max(nw[u], 0), fits(u) ? blocks(ctx[u] + nw[u]) - old : 0, nw[u] < 0 ? old : 0};
+    };
 #pragma unroll
-    for (int u = 0; u < kPlanPer; ++u) {
-      const long long end = (long long)ctx[u] + add[u];
-      fits[u] = end <= cap;
-      const int old = (int)min((long long)a.max_blocks, ((long long)ctx[u] + bs - 1) / bs);
-      mine[u].tok = add[u];
-      mine[u].need = !done[u] && fits[u] ? (int)((end + bs - 1) / bs) - old : 0;
-      mine[u].back = done[u] ? old : 0;
-      sum = sum + mine[u];
-    }
+    for (int u = 0; u < kPlanPer; ++u) sum = sum + part(u);
     Sum3 inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -107,13 +112,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
       if (lane >= o) inc = inc + y;
     }
     __syncthreads();  // the previous round's readers of the shared arrays are done
-    if (lane == 31) wsum[warp] = inc;
+    if (lane == 31) sm.wsum[warp] = inc;
     __syncthreads();
     Sum3 base = carry, all = carry;
 #pragma unroll
     for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w < warp) base = base + wsum[w];
-      all = all + wsum[w];
+      if (w < warp) base = base + sm.wsum[w];
+      all = all + sm.wsum[w];
     }
     Sum3 at{base.tok + inc.tok - sum.tok, base.need + inc.need - sum.need,
             base.back + inc.back - sum.back};
@@ -121,64 +126,60 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 #pragma unroll
     for (int u = 0; u < kPlanPer; ++u) {
       const int i = tid * kPlanPer + u, n = n0 + i;
-      const int cum = at.need + mine[u].need;
-      const bool grant = !done[u] && fits[u] && (mine[u].need == 0 || cum <= count);
-      if (grant && mine[u].need > 0) last_taken = cum;
+      const Sum3 mine = part(u);
+      const int cum = at.need + mine.need;
+      const bool grant = fits(u) && (mine.need == 0 || cum <= count);
+      if (grant && mine.need > 0) last_taken = cum;
       if (n < a.N) {
-        tok0[i] = sat32(at.tok);
-        need0[i] = at.need;
-        back0[i] = at.back;
-        ok[i] = grant;
+        sm.tok0[i] = sat32(at.tok);
+        sm.need0[i] = at.need;
+        sm.back0[i] = at.back;
+        sm.ok[i] = grant;
         if (writer) {
           a.cu_seqlens[n] = sat32(at.tok);
-          a.seq_lens[n] = grant ? (int)((long long)ctx[u] + add[u]) : 0;
+          a.seq_lens[n] = grant ? ctx[u] + nw[u] : 0;
           a.granted[n] = grant;
         }
       }
-      at = at + mine[u];
+      at = at + mine;
     }
     if (tid == 0) {
-      tok0[nn] = sat32(all.tok);
-      need0[nn] = all.need;
-      back0[nn] = all.back;
+      sm.tok0[nn] = sat32(all.tok);
+      sm.need0[nn] = all.need;
+      sm.back0[nn] = all.back;
     }
-    if (last_taken > 0) atomicMax(&taken_s, last_taken);
+    if (last_taken > 0) atomicMax(&sm.taken, last_taken);
     __syncthreads();
 
-    // tokens: a slot in the request's last held block, or in one of its new ones
-    const int t_end = min(tok0[nn], a.T);
-    for (int t = tok0[0] + me; t < t_end; t += stride) {
-      const int i = find(tok0, nn, t), n = n0 + i;
-      const long long pos = (long long)max(__ldg(a.context_lens + n), 0) + (t - tok0[i]);
-      int slot = -1;
-      if (ok[i]) {
-        const int blk = (int)(pos / bs), old = (max(__ldg(a.context_lens + n), 0) + bs - 1) / bs;
-        const int id = blk < old ? a.block_tables[(size_t)n * a.max_blocks + blk]
-                                 : a.free_ring[((long long)head + need0[i] + (blk - old)) % nb];
-        if (id >= 0 && id < nb) slot = (int)((long long)id * bs + (pos - (long long)blk * bs));
+    // The round's tokens, new table entries and released blocks as one list.
+    const int t0 = sm.tok0[0], e0 = sm.need0[0], r0 = sm.back0[0];
+    const long long tokens = max(min(sm.tok0[nn], a.T) - t0, 0);
+    const long long entries = tokens + max(min(sm.need0[nn], count) - e0, 0);
+    const long long all_items = entries + max(min(sm.back0[nn], nb - count) - r0, 0);
+    for (long long x = me; x < all_items; x += stride) {
+      if (x < tokens) {  // a slot in the request's last held block, or in one of its new ones
+        const int t = t0 + (int)x, i = find(sm.tok0, nn, t), n = n0 + i;
+        const int held = max(__ldg(a.context_lens + n), 0);
+        const long long pos = (long long)held + (t - sm.tok0[i]);
+        int slot = -1;
+        if (sm.ok[i]) {
+          const int p = (int)pos, blk = by_bs.div(p), old = blocks(held);
+          const int id = blk < old ? a.block_tables[(size_t)n * a.max_blocks + blk]
+                                   : ring(head + sm.need0[i] + (blk - old));
+          if (id >= 0 && id < nb) slot = id * bs + (p - blk * bs);
+        }
+        a.slot_map[t] = slot;
+        a.positions[t] = sat32(pos);
+      } else if (x < entries) {  // from the front of the ring
+        const int e = e0 + (int)(x - tokens), i = find(sm.need0, nn, e), n = n0 + i;
+        if (sm.ok[i])
+          a.block_tables[(size_t)n * a.max_blocks + blocks(max(__ldg(a.context_lens + n), 0)) + (e - sm.need0[i])] =
+              ring(head + e);
+      } else {  // to the end of the ring (never past its capacity)
+        const int r = r0 + (int)(x - entries), i = find(sm.back0, nn, r), n = n0 + i;
+        const int to = head + count + r;
+        a.free_ring[to >= nb ? to - nb : to] = a.block_tables[(size_t)n * a.max_blocks + (r - sm.back0[i])];
       }
-      a.slot_map[t] = slot;
-      a.positions[t] = sat32(pos);
-      if (stride > 0x7fffffff - t) break;
-    }
-    // new table entries, from the front of the ring
-    const int e_end = min(need0[nn], count);
-    for (int e = need0[0] + me; e < e_end; e += stride) {
-      const int i = find(need0, nn, e), n = n0 + i;
-      if (ok[i]) {
-        const int old = (max(__ldg(a.context_lens + n), 0) + bs - 1) / bs;
-        a.block_tables[(size_t)n * a.max_blocks + old + (e - need0[i])] =
-            a.free_ring[((long long)head + e) % nb];
-      }
-      if (stride > 0x7fffffff - e) break;
-    }
-    // released blocks, to the end of the ring (never past its capacity)
-    const int r_end = min(back0[nn], nb - count);
-    for (int r = back0[0] + me; r < r_end; r += stride) {
-      const int i = find(back0, nn, r), n = n0 + i;
-      a.free_ring[((long long)head + count + r) % nb] =
-          a.block_tables[(size_t)n * a.max_blocks + (r - back0[i])];
-      if (stride > 0x7fffffff - r) break;
     }
     carry = all;
   }
@@ -190,8 +191,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   __syncthreads();
   if (blockIdx.x == 0 && tid == 0) {
     a.cu_seqlens[a.N] = sat32(carry.tok);
-    a.ring_out[0] = (int)(((long long)head + taken_s) % nb);
-    a.ring_out[1] = count - taken_s + min(carry.back, nb - count);
+    const int next = head + sm.taken;
+    a.ring_out[0] = next >= nb ? next - nb : next;
+    a.ring_out[1] = count - sm.taken + min(carry.back, nb - count);
   }
 }
 
@@ -249,12 +251,13 @@ int sm_count() {
 }
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
-  // one thread a token up to two CTAs an SM; requests are scanned by every CTA
+  // one thread a token up to a CTA an SM; requests are scanned by every CTA
   long long ctas = ((long long)(a.T > a.N ? a.T : a.N) + kPlanThreads - 1) / kPlanThreads;
-  const int most = 2 * sm_count();
+  const int most = sm_count();
   if (ctas > most) ctas = most;
   if (ctas < 1) ctas = 1;
-  return launch_early(paged_plan_kernel, dim3((unsigned)ctas), kPlanThreads, 0, stream, a);
+  return launch_early(paged_plan_kernel, dim3((unsigned)ctas), kPlanThreads, 0, stream, a,
+                      FastDiv((unsigned)a.block_size));
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, cudaStream_t stream) {
